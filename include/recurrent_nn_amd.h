@@ -289,6 +289,184 @@ rnn_status rnn_plan_describe(const rnn_plan *plan, char *buf, size_t len);
 /* Release a plan (host memory only).  NULL is a no-op. */
 void rnn_plan_destroy(rnn_plan *plan);
 
+/* ------------------------------------------------------------------------
+ * Operators of a selective-state language model: the layer whose recurrence is
+ * linear with coefficients that depend on the input, its short convolution,
+ * its projections in 8-bit integers, and the scores of what it answers.
+ *
+ * Conventions, besides those above
+ *   - No plan: a descriptor of sizes, strides and types goes with each call and
+ *     is read during it.  Strides count elements; the last dimension of every
+ *     tensor is contiguous.  Tensors need the alignment of their elements only
+ *     (rows whose base and strides are multiples of 16 bytes run faster).
+ *   - sequence_lens is a DEVICE int32 array here, so that a serving loop can
+ *     keep lengths where it computes them and a captured graph can be replayed
+ *     with others; values outside [0, steps] are taken as the nearest of the
+ *     two.  Positions t >= sequence_lens[b] are not read, and their outputs
+ *     are +0.0.
+ *   - A state of a row of length 0 (or of a call with steps = 0) is handed on
+ *     as it came; state_out may be state_in (in place), no other output may
+ *     overlap an input.
+ *   - Sums, states and exponentials are float32 whatever the tensors' type, and
+ *     rounded once (to nearest even) where a value is stored in fewer bits.
+ *   - Every call is stream-ordered, allocates nothing and may be captured.
+ *     Nothing is kept between calls.  Workspaces: device memory, 256-byte
+ *     aligned, of at least the bytes that the matching *_workspace_size
+ *     gives, in use until the stream passes the call.
+ * ---------------------------------------------------------------------- */
+
+/* Element types of the tensors below. */
+typedef enum rnn_dtype {
+    RNN_DTYPE_F32 = 0,
+    RNN_DTYPE_BF16 = 1,
+    RNN_DTYPE_F16 = 2,
+    RNN_DTYPE_I8 = 3
+} rnn_dtype;
+
+#define RNN_CONV_MAX_TAPS 8
+#define RNN_SCAN_MAX_STATES 64
+#define RNN_QUANT_MAX_COLS 131071
+#define RNN_SCORES_MAX_TOP 64
+
+/* x and y [batch, steps, dim]; weight [dim, taps], bias [dim] float32;
+ * states [batch, taps - 1, dim] dense, of x's type. */
+typedef struct rnn_conv_desc {
+    int64_t batch, steps, dim;
+    int64_t x_batch_stride, x_step_stride;
+    int64_t y_batch_stride, y_step_stride;
+    int32_t taps;                      /* 1 to RNN_CONV_MAX_TAPS                      */
+    int32_t silu;                      /* 1: y = v / (1 + exp(-v)) of the sum v       */
+    int32_t dtype;                     /* of x, y and the states: F32, BF16 or F16    */
+} rnn_conv_desc;
+
+/*
+ * rnn_conv_run -- causal convolution of each channel over the last `taps`
+ * steps:  v[b,t,c] = bias[c] + sum_{j < taps} weight[c,j] xx[b, t + j, c], where
+ * xx is state_in (the taps - 1 inputs before the first step, oldest first; NULL
+ * = zeros) followed by x.  state_out (nullable) receives the taps - 1 inputs
+ * before step sequence_lens[b].  One new token is a call with steps = 1.
+ *   bias, state_in, sequence_lens, state_out may be NULL.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, taps
+ *   or dtype outside their ranges, a missing or misaligned tensor, y on x;
+ *   RNN_ERR_UNSUPPORTED for 2^31 or more threads' worth of work.
+ */
+rnn_status rnn_conv_run(const rnn_conv_desc *desc, void *hip_stream, const void *x,
+                        const float *weight, const float *bias, const void *state_in,
+                        const int32_t *sequence_lens, void *y, void *state_out);
+
+/* x, dt, z, y [batch, steps, dim]; B, C [batch, steps, groups, states];
+ * A [dim, states], D and dt_bias [dim] float32; states [batch, dim, states]
+ * float32, dense. */
+typedef struct rnn_scan_desc {
+    int64_t batch, steps, dim, states, groups;   /* channel c reads group c / (dim / groups) */
+    int64_t x_batch_stride, x_step_stride;
+    int64_t dt_batch_stride, dt_step_stride;
+    int64_t z_batch_stride, z_step_stride;
+    int64_t y_batch_stride, y_step_stride;
+    int64_t B_batch_stride, B_step_stride, B_group_stride;
+    int64_t C_batch_stride, C_step_stride, C_group_stride;
+    int32_t dtype;                     /* of x, dt, z, y, B and C: F32, BF16 or F16   */
+    int32_t dt_softplus;               /* 1: step sizes log(1 + exp(dt + dt_bias))    */
+} rnn_scan_desc;
+
+/*
+ * rnn_scan_run -- selective state space scan.  With the step size
+ * s = dt[b,t,c] + dt_bias[c] (through log(1 + exp(.)) with dt_softplus), for
+ * every channel c and state n, t = 0, 1, ...:
+ *     h[n] = exp(s A[c,n]) h[n] + s x[b,t,c] B[b,t,g,n]
+ *     y[b,t,c] = (sum_n C[b,t,g,n] h[n] + D[c] x[b,t,c]) * z / (1 + exp(-z))
+ * with h = state_in (NULL = zeros) before the first step and state_out
+ * (nullable) = h after the last one.  One new token is a call with steps = 1.
+ *   D (no skip), z (no gate), dt_bias, state_in, sequence_lens, state_out may
+ *   be NULL.  A is taken as given (negative for a state that decays).
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
+ *   states outside 1 to RNN_SCAN_MAX_STATES, groups that do not divide dim,
+ *   an unknown dtype, a missing or misaligned tensor, y on an input, a
+ *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for more
+ *   workgroups than one launch takes.
+ */
+rnn_status rnn_scan_workspace_size(const rnn_scan_desc *desc, size_t *bytes);
+rnn_status rnn_scan_run(const rnn_scan_desc *desc, void *hip_stream, void *workspace,
+                        size_t workspace_bytes, const void *x, const void *dt, const float *A,
+                        const void *B, const void *C, const float *D, const void *z,
+                        const float *dt_bias, const float *state_in,
+                        const int32_t *sequence_lens, void *y, float *state_out);
+
+/*
+ * rnn_quantize_rows -- rows of x [rows, cols] to 8-bit integers with one scale
+ * each:  m = max |x|, r = 127 / m, q = x r rounded to the nearest even integer,
+ * scale = m / 127, each operation rounded to float32.  A row with m < 2^-100
+ * gives q = 0 and scale 0; one that holds an infinity or a NaN gives q = 0 and
+ * scale NaN.  q is [rows, q_stride] with q_stride >= cols a multiple of 16 bytes,
+ * 16-byte aligned; columns from cols to q_stride are written as 0.
+ *   The weights of rnn_quant_project are rounded by it once (a row is an output
+ *   channel), activations that several projections share once for each token.
+ *   Errors: RNN_ERR_INVALID_INPUT for sizes below 0, strides or dtype outside
+ *   their ranges, a missing or misaligned tensor; RNN_ERR_UNSUPPORTED for
+ *   2^31 rows or more.
+ */
+rnn_status rnn_quantize_rows(void *hip_stream, int64_t rows, int64_t cols, int32_t dtype,
+                             const void *x, int64_t x_stride, int8_t *q, int64_t q_stride,
+                             float *scale);
+
+typedef struct rnn_quant_desc {
+    int64_t rows, cols, outs;          /* y [rows, outs] = x [rows, cols] . w [outs, cols]^T */
+    int64_t x_stride, w_stride, y_stride;
+    int32_t x_dtype;                   /* F32, BF16, F16: rounded to 8 bits in the call by
+                                          the rule of rnn_quantize_rows; I8: already are   */
+    int32_t y_dtype;                   /* F32, BF16 or F16                             */
+} rnn_quant_desc;
+
+/*
+ * rnn_quant_project -- y[i,o] = (sum_k qx[i,k] w[o,k]) * (x_scale[i] * w_scale[o])
+ * + bias[o], the sum exact in 32-bit integers.  w is int8 [outs, w_stride]: base
+ * and w_stride multiples of 16 bytes, every row readable up to w_stride (the
+ * columns past `cols` may hold anything).  With x_dtype I8, x follows the same
+ * rule with zeros past `cols`, and x_scale [rows] is required; else x_scale
+ * must be NULL.  bias [outs] float32 may be NULL.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
+ *   strides or types outside their ranges, a missing or misaligned tensor, a
+ *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for cols
+ *   above RNN_QUANT_MAX_COLS (beyond it a 32-bit sum can overflow) or for more
+ *   than 2^31 - 1 rows or outs.
+ */
+rnn_status rnn_quant_workspace_size(const rnn_quant_desc *desc, size_t *bytes);
+rnn_status rnn_quant_project(const rnn_quant_desc *desc, void *hip_stream, void *workspace,
+                             size_t workspace_bytes, const void *x, const float *x_scale,
+                             const int8_t *w, const float *w_scale, const float *bias, void *y);
+
+typedef struct rnn_scores_desc {
+    int64_t rows, vocab;               /* logits [rows, vocab]                         */
+    int64_t logits_stride;
+    int32_t dtype;                     /* of the logits: F32, BF16 or F16              */
+    int32_t token_bytes;               /* tokens are int32 (4) or int64 (8)            */
+    int32_t top;                       /* alternatives, 0 to RNN_SCORES_MAX_TOP        */
+} rnn_scores_desc;
+
+/*
+ * rnn_token_scores -- what a row of logits x says of a token k, with
+ * p_v = exp(x_v) / sum_u exp(x_u):  logprob = log p_k;  entropy = -sum p_v log p_v
+ * (0 log 0 = 0);  rank = the number of entries before the token in decreasing
+ * order of x, equal ones in increasing order of their index;  the first `top`
+ * entries of that order as log probabilities (top_logprobs [rows, top]) and
+ * indices (top_ids [rows, top]).  -0 and +0 are equal, NaN is before every number.
+ *   tokens is a DEVICE array [rows]; a token outside [0, vocab) has logprob NaN
+ *   and rank -1 (its row's other outputs are computed).  A row of -inf only, or
+ *   one that holds +inf or NaN, has no distribution: its logprobs and entropy
+ *   are NaN, its rank and top_ids follow the order above.  Where top > vocab the
+ *   rest of top_ids is -1 and of top_logprobs -inf.
+ *   tokens may be NULL if logprob and rank are; any output may be NULL.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, top,
+ *   dtype, token_bytes or stride outside their ranges, a missing or misaligned
+ *   tensor, a workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED
+ *   for 2^31 rows or a vocabulary of 2^31 - 2^16 or more.
+ */
+rnn_status rnn_scores_workspace_size(const rnn_scores_desc *desc, size_t *bytes);
+rnn_status rnn_token_scores(const rnn_scores_desc *desc, void *hip_stream, void *workspace,
+                            size_t workspace_bytes, const void *logits, const void *tokens,
+                            float *logprob, float *entropy, int32_t *rank,
+                            float *top_logprobs, int32_t *top_ids);
+
 /* Thread-local text describing the last non-OK status on this thread. */
 const char *rnn_last_error(void);
 

@@ -5,6 +5,10 @@ This module is the thin binding: the functions named like the C entry points
 marshal arguments and call them; :class:`RNNPlan` adds torch-allocated
 outputs and workspace on the current device and stream.  Every step of the
 operator runs in the HIP library; if the library is missing, nothing runs.
+
+The operators of a selective-state language model (causal_conv,
+selective_scan, quantize_rows, quant_project, token_scores) are in
+:mod:`recurrent_nn_amd.lm` and reached from here; that module imports torch.
 """
 from __future__ import annotations
 
@@ -18,6 +22,18 @@ from ._lib import (RNN_OK, RNN_ERR_INVALID_INPUT, RNN_ERR_UNSUPPORTED, RNN_ERR_D
                    RNN_PROJ_BF16, RNN_PATH_AUTO, RNN_PATH_PERSISTENT, RNN_PATH_PER_STEP,
                    RNN_NOALLOC_SCRATCH_BYTES, RNN_NOALLOC_MAX_LENS_BATCH, STATUS_NAMES,
                    rnn_attrs, rnn_dims)
+
+LM_NAMES = ("causal_conv", "selective_scan", "quantize_rows", "quant_project", "token_scores",
+            "QuantRows", "TokenScores")
+
+
+def __getattr__(name):
+    if name not in LM_NAMES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import lm
+    globals().update((n, getattr(lm, n)) for n in LM_NAMES)
+    return globals()[name]
+
 
 OPS = {"RNN": RNN_OP_RNN, "GRU": RNN_OP_GRU, "LSTM": RNN_OP_LSTM}
 STAGES = ("pack", "projection", "recurrence", "other")

@@ -27,7 +27,16 @@ STATUS_NAMES = {0: "RNN_OK", 1: "RNN_ERR_INVALID_INPUT", 2: "RNN_ERR_UNSUPPORTED
 EXPORTED = ["rnn_plan_create", "rnn_plan_workspace_size", "rnn_run", "rnn_cell_run",
             "rnn_run_noalloc", "rnn_workspace_check",
             "rnn_plan_enable_timing", "rnn_plan_last_timings", "rnn_plan_describe",
-            "rnn_plan_destroy", "rnn_last_error"]
+            "rnn_plan_destroy", "rnn_last_error",
+            "rnn_conv_run", "rnn_scan_workspace_size", "rnn_scan_run", "rnn_quantize_rows",
+            "rnn_quant_workspace_size", "rnn_quant_project", "rnn_scores_workspace_size",
+            "rnn_token_scores"]
+
+RNN_DTYPE_F32, RNN_DTYPE_BF16, RNN_DTYPE_F16, RNN_DTYPE_I8 = range(4)
+RNN_CONV_MAX_TAPS = 8
+RNN_SCAN_MAX_STATES = 64
+RNN_QUANT_MAX_COLS = 131071
+RNN_SCORES_MAX_TOP = 64
 
 
 class rnn_attrs(ctypes.Structure):
@@ -70,6 +79,27 @@ class rnn_dims(ctypes.Structure):
     ]
 
 
+def _struct(name, longs, ints):
+    """A descriptor: int64 fields, then int32 fields."""
+    return type(name, (ctypes.Structure,), {
+        "_fields_": [(f, ctypes.c_int64) for f in longs.split()] +
+                    [(f, ctypes.c_int32) for f in ints.split()]})
+
+
+rnn_conv_desc = _struct(
+    "rnn_conv_desc", "batch steps dim x_batch_stride x_step_stride y_batch_stride y_step_stride",
+    "taps silu dtype")
+rnn_scan_desc = _struct(
+    "rnn_scan_desc", "batch steps dim states groups x_batch_stride x_step_stride dt_batch_stride "
+    "dt_step_stride z_batch_stride z_step_stride y_batch_stride y_step_stride B_batch_stride "
+    "B_step_stride B_group_stride C_batch_stride C_step_stride C_group_stride",
+    "dtype dt_softplus")
+rnn_quant_desc = _struct(
+    "rnn_quant_desc", "rows cols outs x_stride w_stride y_stride", "x_dtype y_dtype")
+rnn_scores_desc = _struct(
+    "rnn_scores_desc", "rows vocab logits_stride", "dtype token_bytes top")
+
+
 _lib = None
 
 
@@ -109,5 +139,17 @@ def load() -> ctypes.CDLL:
     L.rnn_plan_destroy.argtypes = [vp]
     L.rnn_last_error.restype = ctypes.c_char_p
     L.rnn_last_error.argtypes = []
+    i64 = ctypes.c_int64
+    # descriptors are passed by address (ctypes.addressof, or byref)
+    L.rnn_conv_run.argtypes = [vp] * 9
+    L.rnn_scan_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    L.rnn_scan_run.argtypes = [vp, vp, vp, sz] + [vp] * 12
+    L.rnn_quantize_rows.argtypes = [vp, i64, i64, i32, vp, i64, vp, i64, vp]
+    L.rnn_quant_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    L.rnn_quant_project.argtypes = [vp, vp, vp, sz] + [vp] * 6
+    L.rnn_scores_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    L.rnn_token_scores.argtypes = [vp, vp, vp, sz] + [vp] * 7
+    for name in EXPORTED[-8:]:
+        getattr(L, name).restype = i32
     _lib = L
     return L

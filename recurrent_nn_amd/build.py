@@ -49,7 +49,7 @@ HIP_UNITS = ([(f, [], f + ".o") for f in sorted(os.listdir(CSRC))
               if f.endswith(".hip") and f != INST] +
              [(INST, [f"-DRNN_FAMILY={fam}", f"-DRNN_ACT={act}", *FAMILY_FLAGS.get(fam, [])],
                f"recurrence_inst_f{fam}_a{act}.o") for fam, act in INST_UNITS] +
-             [("run.cpp", [], "run.cpp.o")])
+             [("run.cpp", [], "run.cpp.o"), ("lm_run.cpp", [], "lm_run.cpp.o")])
 CXX_UNITS = [("plan.cpp", [], "plan.cpp.o")]
 
 
