@@ -383,7 +383,7 @@ typedef struct rnn_scan_desc {
  *   states outside 1 to RNN_SCAN_MAX_STATES, groups that do not divide dim,
  *   an unknown dtype, a missing or misaligned tensor, y on an input, a
  *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for more
- *   workgroups than one launch takes.
+ *   than 2^31 - 1 channels or steps, or more workgroups than one launch takes.
  */
 rnn_status rnn_scan_workspace_size(const rnn_scan_desc *desc, size_t *bytes);
 rnn_status rnn_scan_run(const rnn_scan_desc *desc, void *hip_stream, void *workspace,

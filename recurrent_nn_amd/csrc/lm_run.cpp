@@ -127,6 +127,8 @@ void check_scan(const rnn_scan_desc *d)
     if ((__int128)d->batch * d->steps > ((__int128)1 << 48) ||
         (__int128)d->batch * d->dim * d->states > ((__int128)1 << 48))
         invalid("sizes out of range");
+    if (d->dim > 0x7fffffff || d->steps > 0x7fffffff)
+        unsupported("more than 2^31 - 1 channels or steps");
 }
 
 void check_quant(const rnn_quant_desc *d)

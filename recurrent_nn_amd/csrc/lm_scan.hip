@@ -3,8 +3,13 @@
 //   s = softplus(dt + dt_bias);  h[n] = exp(s A[n]) h[n] + s x B[n]
 //   y = (sum_n C[n] h[n] + D x) silu(z)
 //
-// First form: a group of lanes as wide as the states (rounded up to a power
-// of two) holds one channel's state, one value a lane, and walks the steps.
+// Bound by the vector unit: a state's step is three products, one exp2 and two
+// additions (24 issue cycles a wave, exp2 is 8 of them), against 8 to 16 bytes
+// a channel's step.  So each exp is computed once, every instruction of the
+// inner loop works on states, and all else (loads, softplus, conversions,
+// skip, gate, stores) is done by other waves of the workgroup.
+#include <type_traits>
+
 #include "lm_common.h"
 
 namespace rnnamd {
@@ -30,77 +35,538 @@ __device__ __forceinline__ float softplus(float v)
     return v != v ? v : l;
 }
 
-template <class T> __global__ __launch_bounds__(256) void scan_kernel(ScanArgs a, int32_t width)
+__device__ __forceinline__ int64_t row_length(const int32_t *lens, int64_t b, int64_t steps)
+{
+    if (!lens)
+        return steps;
+    const int64_t l = lens[b];
+    return l < 0 ? 0 : (l < steps ? l : steps);
+}
+
+// Cross-lane moves within a row of 16 lanes, which the compiler folds into the
+// instruction that uses them.
+template <int CTRL> __device__ __forceinline__ float lanes(float v)
+{
+    return __uint_as_float(__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kBroadcast = 0x150;      // + i: lane i of the row to all its lanes
+constexpr int kXor1 = 0xB1;            // quad_perm [1,0,3,2]
+constexpr int kXor2 = 0x4E;            // quad_perm [2,3,0,1]
+constexpr int kHalfMirror = 0x141;     // lane i from lane 7 - i of its 8
+constexpr int kRor8 = 0x128;           // lane i from lane i xor 8 of its 16
+
+// 16 values a lane, summed over the 16 lanes of a row: lane i gets the sum of
+// value i.  Each stage adds across one bit of the lane number and keeps, in
+// each lane, the half of the values that the lane will end with: 33
+// instructions where 16 full sums take 64.  The first two stages select with
+// the bank mask of the addition itself (a bank is four lanes).  The wait
+// states before a cross-lane read of a fresh register are inside the blocks.
+__device__ __forceinline__ float row_sums(const float (&p)[16], int lane)
+{
+    float r[8], q[4];
+#define RNN_ADD2(out, a, b, perm, mask)                                                     \
+    "v_add_f32_dpp " out ", " a ", " a " " perm " row_mask:0xf bank_mask:0xf\n\t"           \
+    "v_add_f32_dpp " out ", " b ", " b " " perm " row_mask:0xf bank_mask:" mask "\n\t"
+#pragma unroll
+    for (int k = 0; k < 8; k += 4)
+        asm("s_nop 1\n\t"
+            RNN_ADD2("%0", "%4", "%8", "row_ror:8", "0xc")
+            RNN_ADD2("%1", "%5", "%9", "row_ror:8", "0xc")
+            RNN_ADD2("%2", "%6", "%10", "row_ror:8", "0xc")
+            RNN_ADD2("%3", "%7", "%11", "row_ror:8", "0xc")
+            : "=&v"(r[k]), "=&v"(r[k + 1]), "=&v"(r[k + 2]), "=&v"(r[k + 3])
+            : "v"(p[k]), "v"(p[k + 1]), "v"(p[k + 2]), "v"(p[k + 3]), "v"(p[k + 8]),
+              "v"(p[k + 9]), "v"(p[k + 10]), "v"(p[k + 11]));
+    asm("s_nop 1\n\t"
+        RNN_ADD2("%0", "%4", "%8", "row_half_mirror", "0xa")
+        RNN_ADD2("%1", "%5", "%9", "row_half_mirror", "0xa")
+        RNN_ADD2("%2", "%6", "%10", "row_half_mirror", "0xa")
+        RNN_ADD2("%3", "%7", "%11", "row_half_mirror", "0xa")
+        : "=&v"(q[0]), "=&v"(q[1]), "=&v"(q[2]), "=&v"(q[3])
+        : "v"(r[0]), "v"(r[1]), "v"(r[2]), "v"(r[3]), "v"(r[4]), "v"(r[5]), "v"(r[6]), "v"(r[7]));
+#undef RNN_ADD2
+    const bool b1 = lane & 2, b0 = lane & 1;
+    const float u = (b1 ? q[2] : q[0]) + lanes<kXor2>(b1 ? q[0] : q[2]);
+    const float w = (b1 ? q[3] : q[1]) + lanes<kXor2>(b1 ? q[1] : q[3]);
+    return (b0 ? w : u) + lanes<kXor1>(b0 ? u : w);
+}
+
+// Sum over groups of L lanes, in every lane of the group.
+template <int L> __device__ __forceinline__ float group_sum(float v)
+{
+    if (L > 1)
+        v += lanes<kXor1>(v);
+    if (L > 2)
+        v += lanes<kXor2>(v);
+    if (L > 4)
+        v += lanes<kHalfMirror>(v);
+    if (L > 8)
+        v += lanes<kRor8>(v);
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// A few steps (single tokens): bound by the states, read and written once.
+// A lane holds four states, L lanes a channel; 16-byte accesses where the
+// states divide by four.
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kFewSteps = 8;
+
+template <class T, int L> __global__ __launch_bounds__(256) void scan_steps_kernel(ScanArgs a,
+                                                                                 uint32_t row_blocks)
 {
     using raw = typename T::raw;
-    const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) / width;
-    const int32_t n = threadIdx.x % width;
-    const int64_t b = id / a.d.dim, c = id % a.d.dim;
-    if (b >= a.d.batch)
+    const int64_t b = blockIdx.x / row_blocks;
+    const int64_t c = ((int64_t)(blockIdx.x % row_blocks) * 256 + threadIdx.x) / L;
+    const int n0 = threadIdx.x % L * 4;
+    const int64_t steps = a.d.steps, len = row_length(a.lens, b, steps);
+    const int N = (int)a.d.states;
+    if (c >= a.d.dim)
         return;
-    const int64_t steps = a.d.steps, N = a.d.states;
-    int64_t len = steps;
-    if (a.lens) {
-        const int64_t l = a.lens[b];
-        len = l < 0 ? 0 : (l < steps ? l : steps);
+    const bool whole = N % 4 == 0;
+    const int64_t at = (b * a.d.dim + c) * N + n0;
+    const int64_t g = (uint32_t)c / (uint32_t)(a.d.dim / a.d.groups);
+    float h[4] = {}, A[4] = {};
+    if (whole && n0 < N) {
+        if (a.state_in)
+            __builtin_memcpy(h, __builtin_assume_aligned(a.state_in + at, 4), 16);
+        if (len > 0)
+            __builtin_memcpy(A, __builtin_assume_aligned(a.A + c * N + n0, 4), 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < N) {
+                h[i] = a.state_in ? a.state_in[at + i] : 0.0f;
+                A[i] = len > 0 ? a.A[c * N + n0 + i] : 0.0f;
+            }
     }
-    const bool on = n < N;
-    const int64_t g = c / (a.d.dim / a.d.groups);
-    const float A = on && len > 0 ? a.A[c * N + n] * kLog2e : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        A[i] *= kLog2e;
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f;
     const float D = a.D ? a.D[c] : 0.0f;
-    float h = on && a.state_in ? a.state_in[(b * a.d.dim + c) * N + n] : 0.0f;
     const raw *x = (const raw *)a.x + b * a.d.x_batch_stride + c;
     const raw *dt = (const raw *)a.dt + b * a.d.dt_batch_stride + c;
     const raw *z = a.z ? (const raw *)a.z + b * a.d.z_batch_stride + c : nullptr;
-    const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + n;
-    const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + n;
+    const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + n0;
+    const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + n0;
     raw *y = (raw *)a.y + b * a.d.y_batch_stride + c;
     for (int64_t t = 0; t < len; ++t) {
+        float Bv[4] = {}, Cv[4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < N) {
+                Bv[i] = T::load(B[t * a.d.B_step_stride + i]);
+                Cv[i] = T::load(C[t * a.d.C_step_stride + i]);
+            }
         const float xv = T::load(x[t * a.d.x_step_stride]);
+        const raw zv = z ? z[t * a.d.z_step_stride] : raw(0);
         float s = T::load(dt[t * a.d.dt_step_stride]) + bias;
         if (a.d.dt_softplus)
             s = softplus(s);
+        const float sx = s * xv;
         float p = 0.0f;
-        if (on) {
-            h = __builtin_fmaf(__builtin_amdgcn_exp2f(s * A), h,
-                               (s * xv) * T::load(B[t * a.d.B_step_stride]));
-            p = T::load(C[t * a.d.C_step_stride]) * h;
-        }
-        for (int m = width / 2; m > 0; m /= 2)
-            p += __shfl_xor(p, m, 64);
-        if (n == 0) {
-            if (a.D)
-                p = __builtin_fmaf(D, xv, p);
-            if (z)
-                p *= silu(T::load(z[t * a.d.z_step_stride]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < N) {
+                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * A[i]), h[i], sx * Bv[i]);
+                p = __builtin_fmaf(Cv[i], h[i], p);
+            }
+        p = group_sum<L>(p);
+        if (a.D)
+            p = __builtin_fmaf(D, xv, p);
+        if (z)
+            p *= silu(T::load(zv));
+        if (n0 == 0)
             y[t * a.d.y_step_stride] = T::store(p);
-        }
     }
-    if (n == 0)
+    if (n0 == 0)
         for (int64_t t = len; t < steps; ++t)
             y[t * a.d.y_step_stride] = T::store(0.0f);
-    if (on && a.state_out)
-        a.state_out[(b * a.d.dim + c) * N + n] = h;
+    if (!a.state_out)
+        return;
+    if (whole && n0 < N) {
+        __builtin_memcpy(__builtin_assume_aligned(a.state_out + at, 4), h, 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n0 + i < N)
+                a.state_out[at + i] = h[i];
+    }
 }
 
-size_t scan_workspace(const rnn_scan_desc &) { return 0; }
+// ---------------------------------------------------------------------------
+// Many steps
+//
+// A workgroup takes 16 channels of one batch row and walks a span of steps in
+// tiles.  Four waves hold the states: a row of 16 lanes is one channel, lane
+// i has the states i, i + 16, ... (S of them), so that step sizes come by a
+// broadcast within the row that costs nothing, and sums over the states stay
+// within it.  Four other waves prepare the next tile in LDS (step sizes s, s x,
+// B and C in float32, the sums started with D x), and finish the last one
+// (gate, rounding, store); the loads of the tile after next are in flight
+// meanwhile.  One barrier a tile.
+//
+// With too few channels to fill the chip the steps are cut into spans:
+// a first launch finds each span's state from zero and its sum of step sizes,
+// the second starts each span from what the spans before it left,
+//   h := exp(A sum s) h + h_span,  span by span,
+// and has all the outputs.
+// ---------------------------------------------------------------------------
+
+struct Spans {
+    uint32_t per;           // channels of a group of B and C
+    uint32_t per16;         // its workgroups of 16 channels
+    uint32_t groups16;      // all workgroups of a batch row
+    uint32_t count;         // spans of a row
+    int64_t length;         // steps of one, a multiple of the tile
+    float *state;           // [batch, count + 1, dim, states]: each span's own, then state_in
+    float *sum;             // [batch, count, dim]
+};
+
+constexpr int tile_steps(int S) { return S == 1 ? 64 : 32; }
+
+template <class T, int S, bool PAD, bool OUT>
+__global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
+{
+    using raw = typename T::raw;
+    constexpr int TT = tile_steps(S), E = TT / 16;
+    constexpr int SP = TT + 16;         // rows of a wave's four channels in different banks
+    constexpr int BP = TT + 4;          // 16 lanes' 16-byte reads over all banks
+    __shared__ float sh_s[2][16 * SP], sh_sx[2][16 * SP], sh_y[OUT ? 3 : 1][16 * SP];
+    __shared__ __attribute__((aligned(16))) float sh_B[2][16 * S * BP],
+        sh_C[OUT ? 2 : 1][OUT ? 16 * S * BP : 1];
+
+    // Workgroups go to the 8 XCDs in turn: give each XCD adjacent channels, whose
+    // 32-byte pieces of a row share cache lines.
+    const uint32_t total = gridDim.x, xcd = blockIdx.x % 8, q8 = total / 8, r8 = total % 8;
+    const uint32_t id = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+    const uint32_t g = id % sp.groups16 / sp.per16, part = id % sp.groups16 % sp.per16;
+    const int64_t c0 = (int64_t)g * sp.per + part * 16, c_end = (int64_t)(g + 1) * sp.per;
+    const uint32_t span = id / sp.groups16 % sp.count;
+    const int64_t b = id / sp.groups16 / sp.count;
+    const int64_t steps = a.d.steps, dim = a.d.dim;
+    const int N = (int)a.d.states;
+    const int64_t len = row_length(a.lens, b, steps);
+    const int64_t start = span * sp.length;
+    const int64_t stop = start + sp.length < steps ? start + sp.length : steps;
+    const int64_t end = stop < len ? stop : len;
+    const uint32_t tiles = end > start ? (uint32_t)((end - start + TT - 1) / TT) : 0;
+
+    if (threadIdx.x >= 256) {
+        // ---- prepare and finish: thread p has channel p % 16, steps p / 16 + 16 e
+        const int p = threadIdx.x - 256, ch = p % 16, t0 = p / 16;
+        const int64_t c = c0 + ch;
+        const bool on = c < c_end;
+        const int64_t cc = on ? c : c_end - 1;
+        const float bias = a.dt_bias ? a.dt_bias[cc] : 0.0f;
+        const float D = OUT && a.D ? a.D[cc] : 0.0f;
+        const raw *x = (const raw *)a.x + b * a.d.x_batch_stride + cc;
+        const raw *dt = (const raw *)a.dt + b * a.d.dt_batch_stride + cc;
+        const raw *z = OUT && a.z ? (const raw *)a.z + b * a.d.z_batch_stride + cc : nullptr;
+        const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + ch;
+        const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + ch;
+        raw *y = (raw *)a.y + b * a.d.y_batch_stride + cc;
+        raw xr[E], dr[E], zr[E] = {}, Br[E * S], Cr[E * S];
+
+        auto load = [&](uint32_t k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
+                const bool in = t < end;
+                xr[e] = in ? x[t * a.d.x_step_stride] : raw(0);
+                dr[e] = in ? dt[t * a.d.dt_step_stride] : raw(0);
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const bool have = in && (!PAD || ch + 16 * s < N);
+                    Br[e * S + s] = have ? B[t * a.d.B_step_stride + 16 * s] : raw(0);
+                    if (OUT)
+                        Cr[e * S + s] = have ? C[t * a.d.C_step_stride + 16 * s] : raw(0);
+                }
+            }
+        };
+        auto prepare = [&](uint32_t k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int t = t0 + 16 * e;
+                const float xv = T::load(xr[e]);
+                float s = T::load(dr[e]) + bias;
+                if (a.d.dt_softplus)
+                    s = softplus(s);
+                sh_s[k % 2][ch * SP + t] = s;
+                sh_sx[k % 2][ch * SP + t] = s * xv;
+                if (OUT)
+                    sh_y[k % 3][ch * SP + t] = a.D ? D * xv : 0.0f;
+#pragma unroll
+                for (int n = 0; n < S; ++n) {
+                    sh_B[k % 2][(ch + 16 * n) * BP + t] = T::load(Br[e * S + n]);
+                    if (OUT)
+                        sh_C[k % 2][(ch + 16 * n) * BP + t] = T::load(Cr[e * S + n]);
+                }
+            }
+        };
+        auto load_gate = [&](uint32_t k) {
+            if (OUT && z)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
+                    zr[e] = t < end ? z[t * a.d.z_step_stride] : raw(0);
+                }
+        };
+        auto finish = [&](uint32_t k) {
+            if (OUT && on)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
+                    float v = sh_y[k % 3][ch * SP + t0 + 16 * e];
+                    if (z)
+                        v *= silu(T::load(zr[e]));
+                    if (t < end)
+                        y[t * a.d.y_step_stride] = T::store(v);
+                }
+        };
+        if (tiles > 0) {
+            load(0);
+            prepare(0);
+            load(1);
+        }
+        __syncthreads();
+        for (uint32_t k = 0; k < tiles; ++k) {
+            if (k + 1 < tiles)
+                prepare(k + 1);
+            load(k + 2);
+            if (k > 0)
+                finish(k - 1);
+            load_gate(k);
+            __syncthreads();
+        }
+        if (tiles > 0)
+            finish(tiles - 1);
+        if (OUT && on)
+            for (int64_t t = (end > start ? end : start) + t0; t < stop; t += 16)
+                y[t * a.d.y_step_stride] = T::store(0.0f);
+        return;
+    }
+
+    // ---- the states
+    const int lane = threadIdx.x % 16, ch = threadIdx.x / 16;
+    const int64_t c = c0 + ch;
+    const bool on = c < c_end;
+    float h[S], A[S], sums = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int n = lane + 16 * s;
+        h[s] = A[s] = 0.0f;
+        if (!on || (PAD && n >= N))
+            continue;
+        const float rate = len > 0 ? a.A[c * N + n] : 0.0f;
+        if (sp.count > 1) {
+            float *mine = sp.state + (b * (sp.count + 1) * dim + c) * N + n;
+            float *first = mine + (int64_t)sp.count * dim * N;
+            if (span == 0)
+                h[s] = OUT ? *first : a.state_in ? a.state_in[(b * dim + c) * N + n] : 0.0f;
+            if (!OUT && span == 0)
+                *first = h[s];
+            if (OUT && span > 0 && tiles > 0)
+#pragma unroll 8
+                for (uint32_t k = 0; k < span; ++k) {
+                    const float own = mine[(int64_t)k * dim * N];
+                    const float sum = sp.sum[(b * sp.count + k) * dim + c];
+                    // the first span started from state_in
+                    h[s] = k == 0 ? own
+                                  : __builtin_fmaf(__builtin_amdgcn_exp2f(sum * (rate * kLog2e)),
+                                                   h[s], own);
+                }
+        } else if (a.state_in) {
+            h[s] = a.state_in[(b * dim + c) * N + n];
+        }
+        A[s] = rate * kLog2e;
+    }
+    const bool last_on = !PAD || lane + 16 * (S - 1) < N;
+
+    // 16 steps from t of tile k; TAIL: only `left` of them count.
+    auto block = [&](uint32_t k, int t, auto tail, int left) {
+        constexpr bool TAIL = decltype(tail)::value;
+        const float sv = sh_s[k % 2][ch * SP + t + lane];
+        const float xv = sh_sx[k % 2][ch * SP + t + lane];
+        if (!OUT)
+            sums += !TAIL || lane < left ? sv : 0.0f;
+        float p[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float Bq[S][4], Cq[S][4];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                __builtin_memcpy(Bq[s], __builtin_assume_aligned(
+                                            &sh_B[k % 2][(lane + 16 * s) * BP + t + 4 * j], 16), 16);
+                if (OUT)
+                    __builtin_memcpy(Cq[s], __builtin_assume_aligned(
+                                                &sh_C[k % 2][(lane + 16 * s) * BP + t + 4 * j], 16), 16);
+            }
+            auto one = [&](auto step) {
+                constexpr int I = decltype(step)::value;
+                const float sb = lanes<kBroadcast + I>(sv), xb = lanes<kBroadcast + I>(xv);
+                float sum = 0.0f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float e = __builtin_amdgcn_exp2f(sb * A[s]);
+                    const float next = __builtin_fmaf(e, h[s], xb * Bq[s][I % 4]);
+                    h[s] = !TAIL || I < left ? next : h[s];
+                    if (OUT) {
+                        const float v = s == 0 ? Cq[s][I % 4] * h[s]
+                                               : __builtin_fmaf(Cq[s][I % 4], h[s], sum);
+                        sum = PAD && s == S - 1 && !last_on ? sum : v;
+                    }
+                }
+                p[I] = sum;
+            };
+            if (j == 0) {
+                one(std::integral_constant<int, 0>{}), one(std::integral_constant<int, 1>{});
+                one(std::integral_constant<int, 2>{}), one(std::integral_constant<int, 3>{});
+            } else if (j == 1) {
+                one(std::integral_constant<int, 4>{}), one(std::integral_constant<int, 5>{});
+                one(std::integral_constant<int, 6>{}), one(std::integral_constant<int, 7>{});
+            } else if (j == 2) {
+                one(std::integral_constant<int, 8>{}), one(std::integral_constant<int, 9>{});
+                one(std::integral_constant<int, 10>{}), one(std::integral_constant<int, 11>{});
+            } else {
+                one(std::integral_constant<int, 12>{}), one(std::integral_constant<int, 13>{});
+                one(std::integral_constant<int, 14>{}), one(std::integral_constant<int, 15>{});
+            }
+        }
+        if (OUT) {
+            float *out = &sh_y[k % 3][ch * SP + t + lane];
+            *out += row_sums(p, lane);
+        }
+    };
+
+    __syncthreads();
+    for (uint32_t k = 0; k < tiles; ++k) {
+        const int64_t here = end - (start + (int64_t)k * TT);
+        const int count = here < TT ? (int)here : TT;
+        for (int t = 0; t + 16 <= count; t += 16)
+            block(k, t, std::false_type{}, 16);
+        if (count % 16)
+            block(k, count / 16 * 16, std::true_type{}, count % 16);
+        __syncthreads();
+    }
+    if (!OUT) {
+        sums = group_sum<16>(sums);
+        if (on && lane == 0)
+            sp.sum[(b * sp.count + span) * dim + c] = sums;
+    }
+    // The row's last span that has steps (the first one if none has) has its
+    // final state.
+    const bool final = OUT && (end == len ? (span == 0 || start < len) : false);
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int n = lane + 16 * s;
+        if (!on || (PAD && n >= N))
+            continue;
+        if (!OUT)
+            sp.state[((b * (sp.count + 1) + span) * dim + c) * N + n] = h[s];
+        else if (final && a.state_out)
+            a.state_out[(b * dim + c) * N + n] = h[s];
+    }
+}
+
+// Spans of a call: one, unless there are too few workgroups to fill the chip.
+// A second pass costs two thirds of the first again, so it pays from four
+// spans up: with G workgroups of 16 channels, 512 / G spans where that is four
+// or more and each has 128 steps or more (chains of loads start each span).
+static void spans_of(const rnn_scan_desc &d, Spans &sp)
+{
+    const int64_t tile = tile_steps(d.states <= 16 ? 1 : 2);
+    sp.per = (uint32_t)(d.dim / d.groups);
+    sp.per16 = (sp.per + 15) / 16;
+    const int64_t groups16 = sp.per16 * d.groups;
+    sp.groups16 = (uint32_t)groups16;
+    sp.count = 1;
+    sp.length = (d.steps + tile - 1) / tile * tile;
+    if (d.steps <= kFewSteps)
+        return;
+    int64_t count = 512 / (groups16 * d.batch);
+    if (count > d.steps / 128)
+        count = d.steps / 128;
+    if (count < 4)
+        return;
+    sp.length = ((d.steps + count - 1) / count + tile - 1) / tile * tile;
+    sp.count = (uint32_t)((d.steps + sp.length - 1) / sp.length);
+}
+
+size_t scan_workspace(const rnn_scan_desc &d)
+{
+    Spans sp{};
+    spans_of(d, sp);
+    if (sp.count == 1)
+        return 0;
+    return (size_t)d.batch * d.dim * ((sp.count + 1) * d.states + sp.count) * 4;
+}
+
+template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp, hipStream_t s)
+{
+    const dim3 grid((uint32_t)(sp.groups16 * sp.count * a.d.batch)), block(512);
+    const bool pad = a.d.states % 16 != 0;
+    if (sp.count > 1) {
+        if (pad)
+            scan_kernel<T, S, true, false><<<grid, block, 0, s>>>(a, sp);
+        else
+            scan_kernel<T, S, false, false><<<grid, block, 0, s>>>(a, sp);
+        const int rc = (int)hipGetLastError();
+        if (rc)
+            return rc;
+    }
+    if (pad)
+        scan_kernel<T, S, true, true><<<grid, block, 0, s>>>(a, sp);
+    else
+        scan_kernel<T, S, false, true><<<grid, block, 0, s>>>(a, sp);
+    return (int)hipGetLastError();
+}
+
+template <class T, int L> static int steps_go(const ScanArgs &a, hipStream_t s)
+{
+    const int64_t row_blocks = (a.d.dim * L + 255) / 256;
+    if (row_blocks * a.d.batch > 0x7fffffff)
+        return (int)hipErrorInvalidConfiguration;
+    scan_steps_kernel<T, L><<<dim3((uint32_t)(row_blocks * a.d.batch)), dim3(256), 0, s>>>(
+        a, (uint32_t)row_blocks);
+    return (int)hipGetLastError();
+}
+
+template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
+{
+    if (a.d.steps <= kFewSteps) {
+        if (a.d.states <= 4)
+            return steps_go<T, 1>(a, s);
+        if (a.d.states <= 8)
+            return steps_go<T, 2>(a, s);
+        if (a.d.states <= 16)
+            return steps_go<T, 4>(a, s);
+        return a.d.states <= 32 ? steps_go<T, 8>(a, s) : steps_go<T, 16>(a, s);
+    }
+    Spans sp{};
+    spans_of(a.d, sp);
+    if ((__int128)sp.groups16 * sp.count * a.d.batch > 0x7fffffff)
+        return (int)hipErrorInvalidConfiguration;
+    sp.state = (float *)a.workspace;
+    sp.sum = sp.state + (size_t)a.d.batch * (sp.count + 1) * a.d.dim * a.d.states;
+    switch ((a.d.states + 15) / 16) {
+    case 1: return scan_go<T, 1>(a, sp, s);
+    case 2: return scan_go<T, 2>(a, sp, s);
+    case 3: return scan_go<T, 3>(a, sp, s);
+    default: return scan_go<T, 4>(a, sp, s);
+    }
+}
 
 int launch_scan(const ScanArgs &a, hipStream_t s)
 {
-    int32_t width = 1;
-    while (width < a.d.states)
-        width *= 2;
-    const int64_t blocks = (a.d.batch * a.d.dim * width + 255) / 256;
-    if (blocks > 0x7fffffff)
-        return (int)hipErrorInvalidConfiguration;
-    const dim3 grid((uint32_t)blocks), block(256);
     switch (a.d.dtype) {
-    case RNN_DTYPE_F32: scan_kernel<F32><<<grid, block, 0, s>>>(a, width); break;
-    case RNN_DTYPE_BF16: scan_kernel<BF16><<<grid, block, 0, s>>>(a, width); break;
-    default: scan_kernel<F16><<<grid, block, 0, s>>>(a, width); break;
+    case RNN_DTYPE_F32: return scan_type<F32>(a, s);
+    case RNN_DTYPE_BF16: return scan_type<BF16>(a, s);
+    default: return scan_type<F16>(a, s);
     }
-    return (int)hipGetLastError();
 }
 
 }  // namespace rnnamd
