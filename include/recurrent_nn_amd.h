@@ -427,8 +427,8 @@ typedef struct rnn_quant_desc {
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
  *   strides or types outside their ranges, a missing or misaligned tensor, a
  *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for cols
- *   above RNN_QUANT_MAX_COLS (beyond it a 32-bit sum can overflow) or for more
- *   than 2^31 - 1 rows or outs.
+ *   above RNN_QUANT_MAX_COLS (beyond it a 32-bit sum can overflow) or for
+ *   2^31 - 2^16 rows or outs or more.
  */
 rnn_status rnn_quant_workspace_size(const rnn_quant_desc *desc, size_t *bytes);
 rnn_status rnn_quant_project(const rnn_quant_desc *desc, void *hip_stream, void *workspace,

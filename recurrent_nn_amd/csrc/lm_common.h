@@ -59,6 +59,70 @@ __device__ __forceinline__ float silu(float v)
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kLog2e));
 }
 
+// N consecutive elements at an address aligned to one of them (global memory
+// takes wide accesses at any such address).
+template <class T, int N> __device__ __forceinline__ Pack<T, N> load_pack(const typename T::raw *p)
+{
+    Pack<T, N> v;
+    __builtin_memcpy(v.v, p, sizeof(v.v));
+    return v;
+}
+template <class T, int N>
+__device__ __forceinline__ void store_pack(typename T::raw *p, const Pack<T, N> &v)
+{
+    __builtin_memcpy(p, v.v, sizeof(v.v));
+}
+
+// A row's factor to 8 bits and its scale.  max|x| below 2^-100 would bring
+// factors near overflow: such a row counts as zero.
+struct RowScale {
+    float factor, scale;
+};
+__device__ __forceinline__ RowScale row_scale(float most, bool finite)
+{
+    if (!finite)
+        return {0.0f, __uint_as_float(0x7FC00000u)};
+    if (!(most >= 0x1p-100f))
+        return {0.0f, 0.0f};
+    return {127.0f / most, most / 127.0f};
+}
+
+// The largest magnitude over a wave, as bits: magnitudes order as their bits
+// do, infinities and NaN above all finite ones.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+#pragma unroll
+    for (int m = 32; m > 0; m /= 2) {
+        const uint32_t o = __shfl_xor(v, m, 64);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Four values to four 8-bit integers in a word; a row without a factor (zero,
+// or not finite) is 0.  |x factor| <= 127 (1 + 2^-23): rounds to 127 at most.
+__device__ __forceinline__ uint32_t to_8bit(float a, float b, float c, float d, float factor)
+{
+    auto one = [&](float v) { return (uint32_t)(int32_t)__builtin_rintf(v * factor) & 0xFFu; };
+    return factor == 0.0f ? 0u : one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+}
+template <class T> __device__ __forceinline__ uint2 pack_8bit(const Pack<T, 8> &p, float factor)
+{
+    return {to_8bit(T::load(p.v[0]), T::load(p.v[1]), T::load(p.v[2]), T::load(p.v[3]), factor),
+            to_8bit(T::load(p.v[4]), T::load(p.v[5]), T::load(p.v[6]), T::load(p.v[7]), factor)};
+}
+template <class T, int N>
+__device__ __forceinline__ uint32_t pack_max(const Pack<T, N> &p, uint32_t m)
+{
+#pragma unroll
+    for (int v = 0; v < N; ++v) {
+        const uint32_t u = __float_as_uint(T::load(p.v[v])) & 0x7FFFFFFFu;
+        m = u > m ? u : m;
+    }
+    return m;
+}
+
 // ---------------------------------------------------------------------------
 // Launch arguments
 // ---------------------------------------------------------------------------

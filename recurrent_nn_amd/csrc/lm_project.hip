@@ -1,0 +1,447 @@
+// lm_project.hip -- matrix product of 8-bit rows.
+//
+//   y[i,o] = (sum_k qx[i,k] w[o,k]) (x_scale[i] w_scale[o]) + bias[o]
+//
+// Many rows: bound by the matrix unit; tiles of x and w go to LDS by direct
+// loads, 32x32x32 products, the scales in the epilogue.  Few rows: bound by
+// reading w once; it goes from memory to the matrix unit's registers.
+#include <type_traits>
+
+#include "lm_common.h"
+
+namespace rnnamd {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+struct ProjectGo {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale, *bias;
+    void *y;
+    int64_t x_stride, w_stride, y_stride;
+    int32_t rows, outs;
+    int32_t k_end;          // columns, rounded up to 16 (the pitch of both sides reaches it)
+};
+
+// ---------------------------------------------------------------------------
+// Many rows.  A workgroup has BM tokens x BN outputs, WM x WN waves.  A step
+// is 128 columns: a tile row is 128 bytes of LDS, all banks once; its 16-byte
+// pieces are permuted by the row (piece p of row r holds columns 16 (p xor r%8)
+// on) so that the eight rows that one pass of a 16-byte read takes are in
+// different banks.  The permutation is applied to the addresses that the
+// direct loads read from: in LDS they write in order.  Two buffers; a step's
+// loads are in flight during the products of the one before.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void load_to_lds(const int8_t *p, int8_t *lds)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
+                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+
+template <class T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g, uint32_t m_tiles,
+                                                                    uint32_t n_tiles)
+{
+    using raw = typename T::raw;
+    constexpr int THREADS = 64 * WM * WN, KB = 128;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;       // 32 x 32 tiles of a wave
+    constexpr int XP = BM * 8 / THREADS, WP = BN * 8 / THREADS;   // pieces a thread loads
+    constexpr int ON = TN * 32, OP = ON + 4;                  // epilogue: a row of a wave's outputs
+    static_assert(WM * WN * 32 * OP * 4 <= 2 * (BM + BN) * KB, "epilogue fits the tiles' memory");
+    __shared__ __attribute__((aligned(128))) int8_t lds[2 * (BM + BN) * KB];
+
+    // Tiles in bands of 8 tiles of tokens, each XCD (workgroups go to them in
+    // turn) a run of adjacent ones: what runs at a time on an XCD shares rows of
+    // both sides in its L2.
+    const uint32_t total = gridDim.x, xcd = blockIdx.x % 8, q8 = total / 8, r8 = total % 8;
+    const uint32_t id = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
+    const uint32_t band = id / (8 * n_tiles), in = id % (8 * n_tiles);
+    const uint32_t high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+    const int row0 = (int)((band * 8 + in % high) * BM), out0 = (int)(in / high * BN);
+
+    const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const int wm = wave / WN, wn = wave % WN;
+
+    // rows past the end repeat the last one; their outputs are not stored
+    const int8_t *xp[XP], *wp[WP];
+    int kx[XP], kw[WP];
+#pragma unroll
+    for (int i = 0; i < XP; ++i) {
+        const int q = i * THREADS + tid, r = q / 8;
+        const int row = row0 + r < g.rows ? row0 + r : g.rows - 1;
+        kx[i] = (q % 8 ^ (r & 7)) * 16;
+        xp[i] = g.x + (int64_t)row * g.x_stride + kx[i];
+    }
+#pragma unroll
+    for (int i = 0; i < WP; ++i) {
+        const int q = i * THREADS + tid, r = q / 8;
+        const int row = out0 + r < g.outs ? out0 + r : g.outs - 1;
+        kw[i] = (q % 8 ^ (r & 7)) * 16;
+        wp[i] = g.w + (int64_t)row * g.w_stride + kw[i];
+    }
+    auto stage = [&](int buf, int k0) {
+        int8_t *X = lds + buf * (BM + BN) * KB, *W = X + BM * KB;
+        if (k0 + KB <= g.k_end) {
+#pragma unroll
+            for (int i = 0; i < XP; ++i)
+                load_to_lds(xp[i] + k0, X + (i * THREADS + wave * 64) * 16);
+#pragma unroll
+            for (int i = 0; i < WP; ++i)
+                load_to_lds(wp[i] + k0, W + (i * THREADS + wave * 64) * 16);
+        } else {                        // the last columns: zeros behind them
+#pragma unroll
+            for (int i = 0; i < XP; ++i)
+                *(v4i *)(X + (i * THREADS + tid) * 16) =
+                    k0 + kx[i] < g.k_end ? *(const v4i *)(xp[i] + k0) : v4i{};
+#pragma unroll
+            for (int i = 0; i < WP; ++i)
+                *(v4i *)(W + (i * THREADS + tid) * 16) =
+                    k0 + kw[i] < g.k_end ? *(const v4i *)(wp[i] + k0) : v4i{};
+        }
+    };
+
+    v16i acc[TN][TM];
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+            acc[n][m] = v16i{};
+
+    const int steps = (g.k_end + KB - 1) / KB;
+    if (steps > 0)
+        stage(0, 0);
+    __syncthreads();
+    for (int k = 0; k < steps; ++k) {
+        if (k + 1 < steps)
+            stage((k + 1) % 2, (k + 1) * KB);
+        const int8_t *X = lds + k % 2 * (BM + BN) * KB, *W = X + BM * KB;
+        X += (wm * TM * 32 + lane % 32) * KB;
+        W += (wn * TN * 32 + lane % 32) * KB;
+#pragma unroll
+        for (int kk = 0; kk < KB / 32; ++kk) {
+            const int at = ((kk * 2 + lane / 32) ^ (lane & 7)) * 16;
+            v4i fx[TM], fw[TN];
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+                fx[m] = *(const v4i *)(X + m * 32 * KB + at);
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+                fw[n] = *(const v4i *)(W + n * 32 * KB + at);
+#pragma unroll
+            for (int n = 0; n < TN; ++n)
+#pragma unroll
+                for (int m = 0; m < TM; ++m)
+                    acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[n], fx[m], acc[n][m], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+
+    // Epilogue.  A lane holds groups of four outputs of one token; through LDS
+    // (each wave its own part) it gets eight adjacent outputs of a token and
+    // stores them as one piece of a row.
+    int *tile = (int *)lds + wave * 32 * OP;
+    const int o = out0 + wn * ON + lane % (ON / 8) * 8;
+    float ws[8], bs[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        ws[v] = o + v < g.outs ? g.w_scale[o + v] : 0.0f;
+        bs[v] = g.bias && o + v < g.outs ? g.bias[o + v] : 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                *(v4i *)(tile + lane % 32 * OP + n * 32 + 8 * v + 4 * (lane / 32)) =
+                    v4i{acc[n][m][4 * v], acc[n][m][4 * v + 1], acc[n][m][4 * v + 2], acc[n][m][4 * v + 3]};
+        __builtin_amdgcn_wave_barrier();
+        const int t0 = row0 + (wm * TM + m) * 32;
+#pragma unroll
+        for (int r = lane / (ON / 8); r < 32; r += 64 / (ON / 8)) {
+            const v4i *from = (const v4i *)(tile + r * OP + lane % (ON / 8) * 8);
+            const v4i lo = from[0], hi = from[1];
+            const int row = t0 + r;
+            if (row >= g.rows)
+                continue;
+            const float xs = g.x_scale[row];
+            Pack<T, 8> out;
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                float f = (float)(v < 4 ? lo[v % 4] : hi[v % 4]) * (xs * ws[v]);
+                if (g.bias)
+                    f += bs[v];
+                out.v[v] = T::store(f);
+            }
+            raw *y = (raw *)g.y + (int64_t)row * g.y_stride + o;
+            if (o + 8 <= g.outs) {
+                store_pack<T, 8>(y, out);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    if (o + v < g.outs)
+                        y[v] = out.v[v];
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (up to 64, in tiles of 16).  A workgroup has 16 outputs; its four
+// waves take steps of 128 columns in turn and add their sums in LDS.  A lane
+// loads 32 bytes of a weight row, a row's 128 bytes by four lanes, straight
+// into the operands of 16x16x64 products.  With FROM (the rows' type) x is
+// rounded in the call: each workgroup does it for itself, into LDS, while its
+// first weights are on their way; that is less than a launch for few
+// elements.
+// ---------------------------------------------------------------------------
+
+constexpr int kFusedElements = 16384;      // most elements of x for that
+constexpr int kFewRows = 64;
+
+struct NoSource {};
+
+template <class T, class FROM, int TILES>
+__global__ __launch_bounds__(256) void project_rows_kernel(ProjectGo g, const void *x_source,
+                                                          int64_t source_stride, int32_t cols)
+{
+    constexpr bool FUSED = !std::is_same<FROM, NoSource>::value;
+    constexpr int AHEAD = 4;                     // steps of weights in flight
+    extern __shared__ __attribute__((aligned(16))) int8_t q_lds[];   // FUSED: rows of pitch, then scales
+    __shared__ __attribute__((aligned(16))) int sums[3][TILES][256];
+    __shared__ uint32_t row_max[4][FUSED ? 16 : 1];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int out0 = blockIdx.x * 16;
+    const int wrow = out0 + lane % 16 < g.outs ? out0 + lane % 16 : g.outs - 1;
+    const int8_t *w = g.w + (int64_t)wrow * g.w_stride;
+    const int k_lane = lane / 16 * 32;
+    const int steps = (g.k_end + 127) / 128;
+
+    auto piece = [&](const int8_t *p, int k) { return k < g.k_end ? *(const v4i *)(p + k) : v4i{}; };
+    v4i wf[AHEAD][2];
+    auto fetch = [&](int step, v4i (&f)[2]) {
+        const int k = step * 128 + k_lane;
+        f[0] = piece(w, k);
+        f[1] = piece(w, k + 16);
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        fetch(wave + 4 * i, wf[i]);
+
+    const int pitch = steps * 128 + 16;
+    float *q_scale = (float *)(q_lds + g.rows * pitch);
+    if constexpr (FUSED) {
+        using raw = typename FROM::raw;
+        const int packs = steps * 16;            // of 8 elements, zeros past cols
+        auto pack = [&](int r, int i) {
+            const raw *x = (const raw *)x_source + r * source_stride + 8 * i;
+            Pack<FROM, 8> p{};
+            if (8 * i + 8 <= cols) {
+                p = load_pack<FROM, 8>(x);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    if (8 * i + v < cols)
+                        p.v[v] = x[v];
+            }
+            return p;
+        };
+#pragma unroll 4
+        for (int r = 0; r < g.rows; ++r) {
+            uint32_t most = 0;
+            for (int i = threadIdx.x; i < packs; i += 256)
+                most = pack_max<FROM, 8>(pack(r, i), most);
+            most = wave_max(most);
+            if (lane == 0)
+                row_max[wave][r] = most;
+        }
+        __syncthreads();
+        for (int r = 0; r < g.rows; ++r) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                most = row_max[i][r] > most ? row_max[i][r] : most;
+            const RowScale rs = row_scale(__uint_as_float(most), most < kInfBits);
+            for (int i = threadIdx.x; i < packs; i += 256)
+                *(uint2 *)(q_lds + r * pitch + 8 * i) = pack_8bit<FROM>(pack(r, i), rs.factor);
+            if (threadIdx.x == 0)
+                q_scale[r] = rs.scale;
+        }
+        __syncthreads();
+    }
+
+    const int8_t *x[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        const int row = t * 16 + lane % 16 < g.rows ? t * 16 + lane % 16 : g.rows - 1;
+        x[t] = FUSED ? q_lds + row * pitch : g.x + (int64_t)row * g.x_stride;
+    }
+    v4i acc[TILES];
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+        acc[t] = v4i{};
+    for (int s0 = wave; s0 < steps; s0 += 4 * AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const int step = s0 + 4 * i, k = step * 128 + k_lane;
+            if (step < steps) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) {
+                    const v4i a = FUSED ? *(const v4i *)(x[t] + k) : piece(x[t], k);
+                    const v4i b = FUSED ? *(const v4i *)(x[t] + k + 16) : piece(x[t], k + 16);
+                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i][0], a, acc[t], 0, 0, 0);
+                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i][1], b, acc[t], 0, 0, 0);
+                }
+                fetch(step + 4 * AHEAD, wf[i]);
+            }
+        }
+    }
+    // a lane has outputs 4 (lane / 16) .. + 3 of token lane % 16
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+        if (wave > 0)
+            *(v4i *)&sums[wave - 1][t][lane * 4] = acc[t];
+    __syncthreads();
+    if (wave > 0)
+        return;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+        const int row = t * 16 + lane % 16, o = out0 + lane / 16 * 4;
+        v4i sum = acc[t];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            sum += *(const v4i *)&sums[i][t][lane * 4];
+        if (row >= g.rows)
+            continue;
+        const float xs = FUSED ? q_scale[row] : g.x_scale[row];
+        typename T::raw *y = (typename T::raw *)g.y + (int64_t)row * g.y_stride + o;
+        Pack<T, 4> out;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int oo = o + v < g.outs ? o + v : g.outs - 1;
+            float f = (float)sum[v] * (xs * g.w_scale[oo]);
+            if (g.bias)
+                f += g.bias[oo];
+            out.v[v] = T::store(f);
+        }
+        if (o + 4 <= g.outs) {
+            store_pack<T, 4>(y, out);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (o + v < g.outs)
+                    y[v] = out.v[v];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+static int64_t pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+static bool fused(const rnn_quant_desc &d)
+{
+    return d.x_dtype != RNN_DTYPE_I8 && d.rows <= 16 && d.rows * d.cols <= kFusedElements;
+}
+
+size_t project_workspace(const rnn_quant_desc &d)
+{
+    if (d.x_dtype == RNN_DTYPE_I8 || fused(d))
+        return 0;
+    return up256((size_t)d.rows * pitch(d.cols)) + up256((size_t)d.rows * 4);
+}
+
+template <class T, int BM, int BN, int WM, int WN>
+static void tiles_go(const ProjectGo &g, hipStream_t s)
+{
+    const uint32_t m = (uint32_t)((g.rows + (int64_t)BM - 1) / BM);
+    const uint32_t n = (uint32_t)((g.outs + (int64_t)BN - 1) / BN);
+    project_tiles_kernel<T, BM, BN, WM, WN><<<dim3(m * n), dim3(64 * WM * WN), 0, s>>>(g, m, n);
+}
+
+template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &a, hipStream_t s)
+{
+    const dim3 few((uint32_t)((g.outs + (int64_t)15) / 16));
+    const int32_t cols = (int32_t)a.d.cols;
+    if (fused(a.d)) {
+        const size_t lds = (size_t)g.rows * (pitch(cols) + 16) + g.rows * 4;
+        switch (a.d.x_dtype) {
+        case RNN_DTYPE_F32:
+            project_rows_kernel<T, F32, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            break;
+        case RNN_DTYPE_BF16:
+            project_rows_kernel<T, BF16, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            break;
+        default:
+            project_rows_kernel<T, F16, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            break;
+        }
+        return (int)hipGetLastError();
+    }
+    if (g.rows <= kFewRows) {
+        switch ((g.rows + 15) / 16) {
+        case 1: project_rows_kernel<T, NoSource, 1><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
+        case 2: project_rows_kernel<T, NoSource, 2><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
+        case 3: project_rows_kernel<T, NoSource, 3><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
+        default: project_rows_kernel<T, NoSource, 4><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
+        }
+        return (int)hipGetLastError();
+    }
+    // The largest tiles that give most of the 256 compute units one.
+    auto tiles = [&](int64_t bm, int64_t bn) {
+        return (g.rows + bm - 1) / bm * ((g.outs + bn - 1) / bn);
+    };
+    if (tiles(64, 64) > 0x7fffffff)
+        return (int)hipErrorInvalidConfiguration;
+    if (tiles(256, 256) >= 192)
+        tiles_go<T, 256, 256, 2, 4>(g, s);
+    else if (tiles(128, 128) >= 192)
+        tiles_go<T, 128, 128, 2, 2>(g, s);
+    else
+        tiles_go<T, 64, 64, 2, 2>(g, s);
+    return (int)hipGetLastError();
+}
+
+int launch_project(const ProjectArgs &a, hipStream_t s)
+{
+    ProjectGo g{};
+    g.x = (const int8_t *)a.x;
+    g.w = a.w;
+    g.x_scale = a.x_scale;
+    g.w_scale = a.w_scale;
+    g.bias = a.bias;
+    g.y = a.y;
+    g.x_stride = a.d.x_stride;
+    g.w_stride = a.d.w_stride;
+    g.y_stride = a.d.y_stride;
+    g.rows = (int32_t)a.d.rows;
+    g.outs = (int32_t)a.d.outs;
+    g.k_end = (int32_t)((a.d.cols + 15) / 16 * 16);
+    if (a.d.x_dtype != RNN_DTYPE_I8 && !fused(a.d)) {
+        QuantizeArgs q{};
+        q.rows = a.d.rows;
+        q.cols = a.d.cols;
+        q.x_stride = a.d.x_stride;
+        q.q_stride = pitch(a.d.cols);
+        q.dtype = a.d.x_dtype;
+        q.x = a.x;
+        q.q = (int8_t *)a.workspace;
+        q.scale = (float *)((char *)a.workspace + up256((size_t)q.rows * q.q_stride));
+        const int rc = launch_quantize(q, s);
+        if (rc)
+            return rc;
+        g.x = q.q;
+        g.x_scale = q.scale;
+        g.x_stride = q.q_stride;
+    }
+    switch (a.d.y_dtype) {
+    case RNN_DTYPE_F32: return project_go<F32>(g, a, s);
+    case RNN_DTYPE_BF16: return project_go<BF16>(g, a, s);
+    default: return project_go<F16>(g, a, s);
+    }
+}
+
+}  // namespace rnnamd

@@ -144,8 +144,8 @@ void check_quant(const rnn_quant_desc *d)
     if (d->cols > RNN_QUANT_MAX_COLS)
         unsupported("cols above " + std::to_string(RNN_QUANT_MAX_COLS) +
                     ": a 32-bit sum could overflow");
-    if (d->rows > 0x7fffffff || d->outs > 0x7fffffff)
-        unsupported("more than 2^31 - 1 rows or outs");
+    if (d->rows >= ((int64_t)1 << 31) - 65536 || d->outs >= ((int64_t)1 << 31) - 65536)
+        unsupported("2^31 - 2^16 rows or outs or more");
     strides("x", d->rows, d->x_stride, 1, 0, d->cols);
     strides("y", d->rows, d->y_stride, 1, 0, d->outs, true);
     if (d->outs > 0 && (d->w_stride < d->cols || d->w_stride % 16))
