@@ -1,124 +1,461 @@
 // lm_scores.hip -- log probability of a given token, entropy, rank and the
 // most likely alternatives of each row of logits.
 //
-// First form: a workgroup a row; one pass for the maximum, one for the sums
-// and the rank, and one for each alternative.
+//   S = sum exp(x - m),  W = sum exp(x - m) (x - m)
+//   logprob = (x_token - m) - log S,  entropy = log S - W / S   (for any m)
+//
+// Bound by HBM: the logits are read once.  What a thread keeps beside S and W
+// for its elements: the count that precedes the token, and the maxima of eight
+// parts of them.  The k-th largest of the threads' maxima is a bound that at
+// least k elements reach, so that only parts that reach it are read again (k of
+// them and a few, from the caches), and what they hold above it is ordered.
+// Few rows are cut into segments, which a second launch joins.
 #include "lm_common.h"
 
 namespace rnnamd {
 
 // The order of the entries: by value, larger first (NaN before all, -0 equal
-// to +0), then by index, lower first -- as one number, larger first.
+// to +0), then by index, lower first -- as one number, larger first, never 0.
 __device__ __forceinline__ uint64_t order_key(float v, uint32_t index)
 {
     uint32_t u = __float_as_uint(v + 0.0f);
     u = v != v ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
     return ((uint64_t)u << 32) | (0xFFFFFFFFu - index);
 }
-
-__device__ __forceinline__ uint64_t wave_max(uint64_t v)
+__device__ __forceinline__ float key_value(uint64_t key)
 {
-    for (int m = 32; m > 0; m /= 2) {
-        const uint64_t o = __shfl_xor((unsigned long long)v, m, 64);
-        v = o > v ? o : v;
+    const uint32_t u = (uint32_t)(key >> 32);
+    return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
+
+constexpr float kLowest = -3.402823466e38f;
+// Exponents below it count as it: exp is 0 there, and -inf (0 inf = NaN) stays out.
+constexpr float kFar = -1000.0f;
+
+// Sums relative to m, which need not be the maximum: any value near it does.
+struct Sums {
+    float m, sum, cross;
+    __device__ __forceinline__ void rebase(float to)
+    {
+        const float d = __builtin_fmaxf(m - to, kFar);
+        const float scale = __builtin_amdgcn_exp2f(d * kLog2e);
+        cross = __builtin_fmaf(d, sum, cross) * scale;
+        sum *= scale;
+        m = to;
     }
-    return v;
+    __device__ __forceinline__ void join(Sums o)
+    {
+        const float to = __builtin_fmaxf(m, o.m);
+        rebase(to);
+        o.rebase(to);
+        sum += o.sum;
+        cross += o.cross;
+    }
+};
+struct Part {               // of a segment of a row
+    Sums s;
+    uint32_t before;
+};
+
+// The parts of a workgroup's 256 threads together, in every thread.
+__device__ __forceinline__ Part over_workgroup(Part p, Part (&parts)[4])
+{
+#pragma unroll
+    for (int m = 32; m > 0; m /= 2) {
+        const Sums o{__shfl_xor(p.s.m, m, 64), __shfl_xor(p.s.sum, m, 64),
+                     __shfl_xor(p.s.cross, m, 64)};
+        p.s.join(o);
+        p.before += __shfl_xor(p.before, m, 64);
+    }
+    if (threadIdx.x % 64 == 0)
+        parts[threadIdx.x / 64] = p;
+    __syncthreads();
+    p = parts[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        p.s.join(parts[i].s);
+        p.before += parts[i].before;
+    }
+    return p;
 }
 
-template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresArgs a)
-{
-    using raw = typename T::raw;
-    __shared__ uint64_t keys[4];
-    __shared__ float sums[2][4];
-    __shared__ uint32_t counts[4];
-    const int64_t row = blockIdx.x;
-    const uint32_t V = (uint32_t)a.d.vocab;
-    const raw *x = (const raw *)a.logits + row * a.d.logits_stride;
-    const int wave = threadIdx.x / 64;
-    int64_t token = -1;
-    if (a.tokens)
-        token = a.d.token_bytes == 8 ? ((const int64_t *)a.tokens)[row] : ((const int32_t *)a.tokens)[row];
-    const bool known = token >= 0 && token < (int64_t)V;
-    const float mine = known ? T::load(x[token]) : 0.0f;
-    const uint64_t mine_key = known ? order_key(mine, (uint32_t)token) : ~0ull;
+// The best `top` of the keys given to it, in order.  All threads of a
+// workgroup of 256 call its functions together.
+constexpr int kList = 512;
+struct Best {
+    uint64_t *list;         // [kList] of LDS
+    uint64_t *sorted;       // [RNN_SCORES_MAX_TOP]
+    uint32_t *count;
+    int top;
+    uint64_t bound;         // what no longer counts: the last of `top` kept keys
+    uint32_t kept;
 
-    // the largest entry below `below` in the order, over the workgroup
-    auto largest = [&](uint64_t below) {
-        uint64_t best = 0;
-        for (uint32_t v = threadIdx.x; v < V; v += 256) {
-            const uint64_t k = order_key(T::load(x[v]), v);
-            if (k < below && k > best)
-                best = k;
+    __device__ void begin(uint64_t *l, uint64_t *s, uint32_t *c, int k)
+    {
+        list = l, sorted = s, count = c, top = k, bound = 0, kept = 0;
+        if (threadIdx.x == 0)
+            *count = 0;
+        __syncthreads();
+    }
+    __device__ __forceinline__ void offer(uint64_t key, bool on)
+    {
+        if (on && key > bound) {
+            const uint32_t at = atomicAdd(count, 1u);
+            if (at < kList)
+                list[at] = key;
         }
-        best = wave_max(best);
+    }
+    // How many have been offered in all since the last order(); the caller
+    // gives up on what did not fit with forget().
+    __device__ __forceinline__ uint32_t offered()
+    {
         __syncthreads();
-        if (threadIdx.x % 64 == 0)
-            keys[wave] = best;
+        const uint32_t n = *count;
         __syncthreads();
-        for (int i = 0; i < 4; ++i)
-            best = keys[i] > best ? keys[i] : best;
-        return best;
-    };
-    uint64_t key = largest(~0ull);
-    const float most = T::load(x[0xFFFFFFFFu - (uint32_t)key]);
-    float sum = 0.0f, cross = 0.0f;
-    uint32_t before = 0;
-    for (uint32_t v = threadIdx.x; v < V; v += 256) {
-        const float xv = T::load(x[v]);
-        const float e = __builtin_amdgcn_exp2f((xv - most) * kLog2e);
-        sum += e;
-        cross += e == 0.0f ? 0.0f : e * (xv - most);
-        before += order_key(xv, v) > mine_key;
+        return n;
     }
-    for (int m = 32; m > 0; m /= 2) {
-        sum += __shfl_xor(sum, m, 64);
-        cross += __shfl_xor(cross, m, 64);
-        before += __shfl_xor(before, m, 64);
+    __device__ void forget()
+    {
+        if (threadIdx.x == 0)
+            *count = kept;
+        __syncthreads();
     }
-    if (threadIdx.x % 64 == 0) {
-        sums[0][wave] = sum;
-        sums[1][wave] = cross;
-        counts[wave] = before;
+    // Each key's place is the number of larger ones.
+    __device__ void order(uint32_t n)
+    {
+        for (uint32_t i = threadIdx.x; i < n; i += 256) {
+            const uint64_t key = list[i];
+            uint32_t place = 0;
+#pragma unroll 8
+            for (uint32_t j = 0; j < n; ++j)
+                place += list[j] > key;
+            if (place < (uint32_t)top)
+                sorted[place] = key;
+        }
+        __syncthreads();
+        kept = n < (uint32_t)top ? n : (uint32_t)top;
+        if (threadIdx.x < kept)
+            list[threadIdx.x] = sorted[threadIdx.x];
+        if (threadIdx.x == 0)
+            *count = kept;
+        if (n >= (uint32_t)top)
+            bound = sorted[top - 1];
+        __syncthreads();
     }
-    __syncthreads();
-    sum = sums[0][0] + sums[0][1] + sums[0][2] + sums[0][3];
-    cross = sums[1][0] + sums[1][1] + sums[1][2] + sums[1][3];
-    before = counts[0] + counts[1] + counts[2] + counts[3];
-    const float lse = __builtin_amdgcn_logf(sum) * kLn2;
+};
+
+template <class T> __device__ __forceinline__ Pack<T, 8> logits_pack(const typename T::raw *x,
+                                                                    uint32_t i, uint32_t V)
+{
+    if (8 * i + 8 <= V)
+        return load_pack<T, 8>(x + 8 * (int64_t)i);
+    Pack<T, 8> p;
+#pragma unroll
+    for (uint32_t v = 0; v < 8; ++v)
+        p.v[v] = 8 * i + v < V ? x[8 * (int64_t)i + v] : T::store(-__builtin_inff());
+    return p;
+}
+
+struct Token {
+    int64_t id;
+    bool known;
+    float value;
+};
+template <class T> __device__ __forceinline__ Token token_of(const ScoresArgs &a, int64_t row,
+                                                            const typename T::raw *x)
+{
+    Token t{-1, false, 0.0f};
+    if (a.tokens)
+        t.id = a.d.token_bytes == 8 ? ((const int64_t *)a.tokens)[row] : ((const int32_t *)a.tokens)[row];
+    t.known = t.id >= 0 && t.id < a.d.vocab;
+    if (t.known)
+        t.value = T::load(x[t.id]);
+    return t;
+}
+
+// A row's outputs from its sums and its ordered best keys.
+__device__ __forceinline__ void put_scores(const ScoresArgs &a, int64_t row, const Part &p,
+                                           const Token &t, const uint64_t *sorted, uint32_t kept)
+{
+    const float lse = __builtin_amdgcn_logf(p.s.sum) * kLn2;
     if (threadIdx.x == 0) {
         if (a.logprob)
-            a.logprob[row] = known ? (mine - most) - lse : __uint_as_float(0x7FC00000u);
+            a.logprob[row] = t.known ? (t.value - p.s.m) - lse : __uint_as_float(0x7FC00000u);
         if (a.entropy)
-            a.entropy[row] = lse - cross / sum;
+            a.entropy[row] = lse - p.s.cross / p.s.sum;
         if (a.rank)
-            a.rank[row] = known ? (int32_t)before : -1;
+            a.rank[row] = t.known ? (int32_t)p.before : -1;
     }
-    for (int32_t j = 0; j < a.d.top; ++j) {
-        const bool any = j < (int64_t)V;
-        if (any && j > 0)
-            key = largest(key);
-        if (threadIdx.x == 0) {
-            const uint32_t at = 0xFFFFFFFFu - (uint32_t)key;
-            if (a.top_logprobs)
-                a.top_logprobs[row * a.d.top + j] =
-                    any ? (T::load(x[at]) - most) - lse : -__builtin_inff();
-            if (a.top_ids)
-                a.top_ids[row * a.d.top + j] = any ? (int32_t)at : -1;
-        }
+    const int j = threadIdx.x;
+    if (j < a.d.top) {
+        const bool have = (uint32_t)j < kept;
+        const uint64_t key = have ? sorted[j] : 0;
+        if (a.top_logprobs)
+            a.top_logprobs[row * a.d.top + j] =
+                have ? (key_value(key) - p.s.m) - lse : -__builtin_inff();
+        if (a.top_ids)
+            a.top_ids[row * a.d.top + j] = have ? (int32_t)key_index(key) : -1;
     }
 }
 
-size_t scores_workspace(const rnn_scores_desc &) { return 0; }
+// One segment of a row: packs [first, last) of 8 elements.
+template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresArgs a,
+                                                                      uint32_t segments,
+                                                                      uint32_t segment_packs)
+{
+    using raw = typename T::raw;
+    constexpr int PARTS = 8;
+    __shared__ uint64_t list[kList], sorted[RNN_SCORES_MAX_TOP];
+    __shared__ __attribute__((aligned(16))) float maxima[256];
+    __shared__ uint32_t count, items[256];
+    __shared__ Part parts[4];
+    __shared__ float bound_value;
+    const uint32_t tid = threadIdx.x;
+    const int64_t row = blockIdx.x / segments;
+    const uint32_t segment = blockIdx.x % segments;
+    const uint32_t V = (uint32_t)a.d.vocab, all = (V + 7) / 8;
+    const uint32_t first = segment * segment_packs;
+    const uint32_t last = first + segment_packs < all ? first + segment_packs : all;
+    const raw *x = (const raw *)a.logits + row * a.d.logits_stride;
+    const Token tk = token_of<T>(a, row, x);
+    const float mine = tk.value;
+    const bool unordered = mine != mine;
+
+    // What counts as before the token: packs before the token's own by
+    // !(x <= lower), lower the next value below it; packs from its own on by
+    // !(x <= mine).  Its own pack's equal entries before it are added below.
+    // (A NaN is preceded by the NaN of lower index only; -inf by all of them.)
+    const uint32_t token_pack = tk.known ? (uint32_t)(tk.id / 8) : 0;
+    float lower, upper = unordered ? __builtin_inff() : mine;
+    {
+        const uint32_t u = __float_as_uint(mine);
+        lower = mine == 0.0f ? -__uint_as_float(1u)
+                             : __uint_as_float((u & 0x80000000u) ? u + 1u : u - 1u);
+        if (unordered)
+            lower = __builtin_inff();
+        else if (mine == -__builtin_inff())
+            lower = __uint_as_float(0x7FC00000u);
+    }
+    const uint32_t upper_counts = unordered ? 0u : ~0u;
+
+    Part p{{kLowest, 0.0f, 0.0f}, 0};
+    float most[PARTS];
+    const uint32_t mine_packs = last > first + tid ? (last - first - tid + 255) / 256 : 0;
+    const uint32_t part_packs = ((last - first + 255) / 256 + PARTS - 1) / PARTS;
+    auto one = [&](const Pack<T, 8> &pk, uint32_t i, float &top_of_part) {
+        float f[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            f[v] = T::load(pk.v[v]);
+        const float pm = __builtin_fmaxf(
+            __builtin_fmaxf(__builtin_fmaxf(f[0], f[1]), __builtin_fmaxf(f[2], f[3])),
+            __builtin_fmaxf(__builtin_fmaxf(f[4], f[5]), __builtin_fmaxf(f[6], f[7])));
+        top_of_part = __builtin_fmaxf(top_of_part, pm);
+        if (pm > p.s.m + 8.0f)          // rare after the first pack
+            p.s.rebase(pm);
+        const bool below = i < token_pack;
+        const float edge = below ? lower : upper;
+        uint32_t n = 0;
+        float e[8];
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const float d = f[v] - p.s.m;
+            e[v] = __builtin_amdgcn_exp2f(d * kLog2e);
+            p.s.cross = __builtin_fmaf(e[v], __builtin_fmaxf(d, kFar), p.s.cross);
+            n += !(f[v] <= edge);
+        }
+        p.s.sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        p.before += n & (below ? ~0u : upper_counts);
+    };
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s) {
+        most[s] = -__builtin_inff();
+        const uint32_t from = s * part_packs;
+        const uint32_t to = from + part_packs < mine_packs ? from + part_packs : mine_packs;
+        uint32_t j = from;
+        for (; j + 4 <= to; j += 4) {
+            Pack<T, 8> pk[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                pk[u] = logits_pack<T>(x, first + tid + 256 * (j + u), V);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                one(pk[u], first + tid + 256 * (j + u), most[s]);
+        }
+        for (; j < to; ++j)
+            one(logits_pack<T>(x, first + tid + 256 * j, V), first + tid + 256 * j, most[s]);
+    }
+    if (tid == 0 && tk.known && token_pack >= first && token_pack < last)
+        for (uint32_t v = token_pack * 8; v < (uint32_t)tk.id; ++v) {
+            const float f = T::load(x[v]);
+            p.before += f == mine || (unordered && f != f);
+        }
+
+    // over the workgroup
+    float mx = most[0];
+#pragma unroll
+    for (int s = 1; s < PARTS; ++s)
+        mx = __builtin_fmaxf(mx, most[s]);
+    maxima[tid] = mx;
+    p = over_workgroup(p, parts);
+
+    const int top = a.d.top;
+    Best best;
+    best.begin(list, sorted, &count, top);
+    if (top > 0) {
+        // the bound: the top-th of the threads' maxima, ties in any order
+        uint32_t place = 0;
+        for (int j = 0; j < 256; j += 4) {
+            const float4 o = *(const float4 *)&maxima[j];
+            place += o.x > mx || (o.x == mx && j + 0 < (int)tid);
+            place += o.y > mx || (o.y == mx && j + 1 < (int)tid);
+            place += o.z > mx || (o.z == mx && j + 2 < (int)tid);
+            place += o.w > mx || (o.w == mx && j + 3 < (int)tid);
+        }
+        if (place == (uint32_t)top - 1)
+            bound_value = mx;
+        __syncthreads();
+        // (m may exceed no element: NaN and infinities show in the sum)
+        const bool odd = !(p.s.sum < __builtin_inff());
+        const float edge = bound_value;
+#pragma unroll
+        for (int s = 0; s < PARTS; ++s)
+            if (!odd && most[s] >= edge) {
+                const uint32_t at = atomicAdd(&count, 1u);
+                if (at < 256)
+                    items[at] = s * 256 + tid;
+            }
+        uint32_t n = best.offered();
+        best.forget();
+        const bool few = !odd && n <= 256;
+        const uint32_t packs = few ? n * part_packs : last - first;
+        auto offer = [&](const Pack<T, 8> &pk, uint32_t i, bool on, int v) {
+            const float f = T::load(pk.v[v]);
+            best.offer(order_key(f, 8 * i + v),
+                       on && 8 * i + v < V && (odd || f >= edge));
+        };
+        for (uint32_t base = 0; base < packs; base += 256) {
+            const uint32_t q = base + tid;
+            bool on = q < packs;
+            uint32_t i = first + q;
+            if (few && on) {
+                const uint32_t item = items[q / part_packs];
+                const uint32_t j = item / 256 * part_packs + q % part_packs;
+                i = first + item % 256 + 256 * j;
+                on = i < last;
+            }
+            Pack<T, 8> pk{};
+            if (on)
+                pk = logits_pack<T>(x, i, V);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                offer(pk, i, on, v);
+            n = best.offered();
+            if (n > kList) {            // too many at once: an eighth of them at a time
+                best.forget();
+#pragma unroll 1
+                for (int v = 0; v < 8; ++v) {
+                    const uint64_t key = order_key(T::load(pk.v[0]), 8 * i + v);
+                    best.offer(key, on && 8 * i + v < V && (odd || T::load(pk.v[0]) >= edge));
+                    n = best.offered();
+                    best.order(n);
+#pragma unroll
+                    for (int u = 0; u < 7; ++u)
+                        pk.v[u] = pk.v[u + 1];
+                }
+            } else if (n > kList / 2) {
+                best.order(n);
+            }
+        }
+        n = best.offered();
+        best.order(n);
+    }
+    if (segments == 1) {
+        put_scores(a, row, p, tk, sorted, best.kept);
+        return;
+    }
+    uint64_t *keys = (uint64_t *)a.workspace + (int64_t)blockIdx.x * top;
+    Part *out = (Part *)((uint64_t *)a.workspace + (int64_t)gridDim.x * top) + blockIdx.x;
+    if (tid == 0)
+        *out = p;
+    if (tid < (uint32_t)top)
+        keys[tid] = tid < best.kept ? sorted[tid] : 0;
+}
+
+// The segments of a row together.
+template <class T> __global__ __launch_bounds__(256) void scores_join_kernel(ScoresArgs a,
+                                                                           uint32_t segments)
+{
+    __shared__ uint64_t list[kList], sorted[RNN_SCORES_MAX_TOP];
+    __shared__ uint32_t count;
+    __shared__ Part parts[4];
+    const int64_t row = blockIdx.x;
+    const uint32_t top = (uint32_t)a.d.top, n_keys = segments * top;
+    const uint64_t *keys = (const uint64_t *)a.workspace + row * n_keys;
+    const Part *in = (const Part *)((const uint64_t *)a.workspace + (int64_t)gridDim.x * n_keys) +
+                     row * segments;
+    const Token tk = token_of<T>(a, row, (const typename T::raw *)a.logits + row * a.d.logits_stride);
+    Best best;
+    best.begin(list, sorted, &count, (int)top);
+    for (uint32_t base = 0; base < n_keys; base += 256) {
+        const uint32_t q = base + threadIdx.x;
+        best.offer(q < n_keys ? keys[q] : 0, q < n_keys);
+        const uint32_t n = best.offered();
+        if (n > kList - 256)
+            best.order(n);
+    }
+    if (top > 0)
+        best.order(best.offered());
+    Part p{{kLowest, 0.0f, 0.0f}, 0};
+    for (uint32_t i = threadIdx.x; i < segments; i += 256) {
+        p.s.join(in[i].s);
+        p.before += in[i].before;
+    }
+    p = over_workgroup(p, parts);
+    put_scores(a, row, p, tk, sorted, best.kept);
+}
+
+// Segments of a row: as many as bring about 512 workgroups, of 4096 elements
+// or more each.
+static uint32_t segments_of(const rnn_scores_desc &d, uint32_t &packs)
+{
+    const int64_t all = (d.vocab + 7) / 8;
+    int64_t n = 512 / d.rows;
+    if (n > (all + 511) / 512)
+        n = (all + 511) / 512;
+    if (n < 1)
+        n = 1;
+    packs = (uint32_t)((all + n - 1) / n);
+    return (uint32_t)((all + packs - 1) / packs);
+}
+
+size_t scores_workspace(const rnn_scores_desc &d)
+{
+    uint32_t packs;
+    const uint32_t segments = segments_of(d, packs);
+    return segments > 1 ? (size_t)d.rows * segments * (sizeof(Part) + 8 * (size_t)d.top) : 0;
+}
+
+template <class T> static int scores_go(const ScoresArgs &a, hipStream_t s)
+{
+    uint32_t packs;
+    const uint32_t segments = segments_of(a.d, packs);
+    scores_kernel<T><<<dim3((uint32_t)a.d.rows * segments), dim3(256), 0, s>>>(a, segments, packs);
+    const int rc = (int)hipGetLastError();
+    if (rc || segments == 1)
+        return rc;
+    scores_join_kernel<T><<<dim3((uint32_t)a.d.rows), dim3(256), 0, s>>>(a, segments);
+    return (int)hipGetLastError();
+}
 
 int launch_scores(const ScoresArgs &a, hipStream_t s)
 {
-    const dim3 grid((uint32_t)a.d.rows), block(256);
     switch (a.d.dtype) {
-    case RNN_DTYPE_F32: scores_kernel<F32><<<grid, block, 0, s>>>(a); break;
-    case RNN_DTYPE_BF16: scores_kernel<BF16><<<grid, block, 0, s>>>(a); break;
-    default: scores_kernel<F16><<<grid, block, 0, s>>>(a); break;
+    case RNN_DTYPE_F32: return scores_go<F32>(a, s);
+    case RNN_DTYPE_BF16: return scores_go<BF16>(a, s);
+    default: return scores_go<F16>(a, s);
     }
-    return (int)hipGetLastError();
 }
 
 }  // namespace rnnamd
