@@ -73,6 +73,28 @@ __device__ __forceinline__ void store_pack(typename T::raw *p, const Pack<T, N> 
     __builtin_memcpy(p, v.v, sizeof(v.v));
 }
 
+// Four elements as loaded, in whole words: taken apart where they are used, so
+// that a loop can carry them while the load is in flight.
+template <class T> struct Words4 {
+    static constexpr int kWords = sizeof(typename T::raw);      // 4 elements: 2 or 4 words
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int v) const
+    {
+        if constexpr (kWords == 4)
+            return T::load(w[v]);
+        else
+            return T::load((typename T::raw)(v % 2 ? w[v / 2] >> 16 : w[v / 2] & 0xFFFFu));
+    }
+    __device__ __forceinline__ void load(const typename T::raw *p) { __builtin_memcpy(w, p, sizeof(w)); }
+    __device__ __forceinline__ void set(int v, typename T::raw r)
+    {
+        if constexpr (kWords == 4)
+            w[v] = r;
+        else
+            w[v / 2] = v % 2 ? w[v / 2] | (uint32_t)r << 16 : (uint32_t)r;
+    }
+};
+
 // A row's factor to 8 bits and its scale.  max|x| below 2^-100 would bring
 // factors near overflow: such a row counts as zero.
 struct RowScale {

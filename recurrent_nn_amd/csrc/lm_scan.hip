@@ -16,23 +16,21 @@ namespace rnnamd {
 
 // log(1 + exp(v)) = max(v, 0) + log1p(w), w = exp(-|v|) in (0, 1].  With
 // q = w / (2 + w), log1p(w) = 2 atanh(q) = 2 q (1 + q^2/3 + q^4/5 + ...): no
-// cancellation for small w; q <= 1/3, so nine terms reach 2^-29.
+// cancellation for small w; q <= 1/3, so seven terms reach 2^-26.  (NaN goes
+// through w, infinities through the maximum.)
 __device__ __forceinline__ float softplus(float v)
 {
     const float w = __builtin_amdgcn_exp2f(-__builtin_fabsf(v) * kLog2e);
     const float q = w * __builtin_amdgcn_rcpf(2.0f + w);
     const float r = q * q;
-    float p = 1.0f / 17.0f;
-    p = __builtin_fmaf(p, r, 1.0f / 15.0f);
-    p = __builtin_fmaf(p, r, 1.0f / 13.0f);
+    float p = 1.0f / 13.0f;
     p = __builtin_fmaf(p, r, 1.0f / 11.0f);
     p = __builtin_fmaf(p, r, 1.0f / 9.0f);
     p = __builtin_fmaf(p, r, 1.0f / 7.0f);
     p = __builtin_fmaf(p, r, 1.0f / 5.0f);
     p = __builtin_fmaf(p, r, 1.0f / 3.0f);
     p = __builtin_fmaf(p, r, 1.0f);
-    const float l = __builtin_fmaf(q + q, p, v > 0.0f ? v : 0.0f);
-    return v != v ? v : l;
+    return __builtin_fmaf(q + q, p, __builtin_fmaxf(v, 0.0f));
 }
 
 __device__ __forceinline__ int64_t row_length(const int32_t *lens, int64_t b, int64_t steps)
@@ -226,14 +224,19 @@ struct Spans {
     float *sum;             // [batch, count, dim]
 };
 
-constexpr int tile_steps(int S) { return S == 1 ? 64 : 32; }
+constexpr int kTile = 64;
 
-template <class T, int S, bool PAD, bool OUT>
+// WHOLE: 16 channels in every workgroup and states in whole sixteens, so that
+// four adjacent ones are one load.  Else elements beyond the last are loaded as
+// the last (no load depends on a condition: it would be waited for on the spot)
+// and left out of sums and stores.
+template <class T, int S, bool WHOLE, bool OUT>
 __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
 {
     using raw = typename T::raw;
-    constexpr int TT = tile_steps(S), E = TT / 16;
-    constexpr int SP = TT + 16;         // rows of a wave's four channels in different banks
+    constexpr bool PAD = !WHOLE;
+    constexpr int TT = kTile;
+    constexpr int SP = TT + 20;         // 4 x 4 channels of 16 steps over all banks
     constexpr int BP = TT + 4;          // 16 lanes' 16-byte reads over all banks
     __shared__ float sh_s[2][16 * SP], sh_sx[2][16 * SP], sh_y[OUT ? 3 : 1][16 * SP];
     __shared__ __attribute__((aligned(16))) float sh_B[2][16 * S * BP],
@@ -256,76 +259,137 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
     const uint32_t tiles = end > start ? (uint32_t)((end - start + TT - 1) / TT) : 0;
 
     if (threadIdx.x >= 256) {
-        // ---- prepare and finish: thread p has channel p % 16, steps p / 16 + 16 e
-        const int p = threadIdx.x - 256, ch = p % 16, t0 = p / 16;
+        // ---- prepare and finish: thread p has step p / 4 of a tile, channels (and
+        // states, of each sixteen) 4 (p % 4) to + 3
+        using P4 = Words4<T>;
+        const int p = threadIdx.x - 256, ch = p % 4 * 4, t0 = p / 4;
         const int64_t c = c0 + ch;
-        const bool on = c < c_end;
-        const int64_t cc = on ? c : c_end - 1;
-        const float bias = a.dt_bias ? a.dt_bias[cc] : 0.0f;
-        const float D = OUT && a.D ? a.D[cc] : 0.0f;
-        const raw *x = (const raw *)a.x + b * a.d.x_batch_stride + cc;
-        const raw *dt = (const raw *)a.dt + b * a.d.dt_batch_stride + cc;
-        const raw *z = OUT && a.z ? (const raw *)a.z + b * a.d.z_batch_stride + cc : nullptr;
-        const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + ch;
-        const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + ch;
-        raw *y = (raw *)a.y + b * a.d.y_batch_stride + cc;
-        raw xr[E], dr[E], zr[E] = {}, Br[E * S], Cr[E * S];
+        auto channel = [&](int v) { return WHOLE || c + v < c_end ? c + v : c_end - 1; };
+        float bias[4], D[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            bias[v] = a.dt_bias ? a.dt_bias[channel(v)] : 0.0f;
+            D[v] = OUT && a.D ? a.D[channel(v)] : 0.0f;
+        }
+        // Rows of the thread's step in the tile that is loaded next, beyond the end
+        // the last one's.
+        struct Row {
+            const raw *at;
+            int64_t step;
+            __device__ __forceinline__ void go(int64_t steps) { at += steps * step; }
+        };
+        Row x{(const raw *)a.x + b * a.d.x_batch_stride, a.d.x_step_stride};
+        Row dt{(const raw *)a.dt + b * a.d.dt_batch_stride, a.d.dt_step_stride};
+        // without a gate x is loaded in its place, and not used
+        Row z = a.z ? Row{(const raw *)a.z + b * a.d.z_batch_stride, a.d.z_step_stride} : x;
+        Row B{(const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride, a.d.B_step_stride};
+        Row C{(const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride, a.d.C_step_stride};
+        raw *y = (raw *)a.y + b * a.d.y_batch_stride + (start + t0) * a.d.y_step_stride + c;
+        const int64_t t_first = start + t0 < end ? start + t0 : end - 1;
+        x.go(t_first), dt.go(t_first), z.go(t_first), B.go(t_first), C.go(t_first);
+        // from tile k to the next: a whole tile of steps, fewer before the end
+        auto beyond = [&](uint32_t k) { return start + (int64_t)(k + 2) * TT > end; };
+        auto to_next = [&](uint32_t k) {
+            const int64_t now = start + (int64_t)k * TT + t0, next = now + TT;
+            return (next < end ? next : end - 1) - (now < end ? now : end - 1);
+        };
+        P4 xr, dr, zr{}, Br[S], Cr[S];
 
+        auto four_channels = [&](const raw *row) {
+            P4 f;
+            if (WHOLE) {
+                f.load(row + c);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    f.set(v, row[channel(v)]);
+            }
+            return f;
+        };
+        auto four_states = [&](const raw *row, int s) {
+            P4 f;
+            if (WHOLE) {
+                f.load(row + 16 * s + ch);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    f.set(v, row[16 * s + ch + v < N ? 16 * s + ch + v : N - 1]);
+            }
+            return f;
+        };
         auto load = [&](uint32_t k) {
+            xr = four_channels(x.at);
+            dr = four_channels(dt.at);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
-                const bool in = t < end;
-                xr[e] = in ? x[t * a.d.x_step_stride] : raw(0);
-                dr[e] = in ? dt[t * a.d.dt_step_stride] : raw(0);
-#pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const bool have = in && (!PAD || ch + 16 * s < N);
-                    Br[e * S + s] = have ? B[t * a.d.B_step_stride + 16 * s] : raw(0);
-                    if (OUT)
-                        Cr[e * S + s] = have ? C[t * a.d.C_step_stride + 16 * s] : raw(0);
-                }
+            for (int s = 0; s < S; ++s) {
+                Br[s] = four_states(B.at, s);
+                if (OUT)
+                    Cr[s] = four_states(C.at, s);
+            }
+            if (!beyond(k)) {
+                x.go(TT), dt.go(TT), B.go(TT), C.go(TT);
+            } else {
+                const int64_t n = to_next(k);
+                x.go(n), dt.go(n), B.go(n), C.go(n);
             }
         };
         auto prepare = [&](uint32_t k) {
+            float s[4];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int t = t0 + 16 * e;
-                const float xv = T::load(xr[e]);
-                float s = T::load(dr[e]) + bias;
-                if (a.d.dt_softplus)
-                    s = softplus(s);
-                sh_s[k % 2][ch * SP + t] = s;
-                sh_sx[k % 2][ch * SP + t] = s * xv;
+            for (int v = 0; v < 4; ++v)
+                s[v] = dr.get(v) + bias[v];
+            if (a.d.dt_softplus)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    s[v] = softplus(s[v]);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int at = (ch + v) * SP + t0;
+                const float xv = xr.get(v);
+                sh_s[k % 2][at] = s[v];
+                sh_sx[k % 2][at] = s[v] * xv;
                 if (OUT)
-                    sh_y[k % 3][ch * SP + t] = a.D ? D * xv : 0.0f;
+                    sh_y[k % 3][at] = a.D ? D[v] * xv : 0.0f;
 #pragma unroll
                 for (int n = 0; n < S; ++n) {
-                    sh_B[k % 2][(ch + 16 * n) * BP + t] = T::load(Br[e * S + n]);
+                    sh_B[k % 2][(ch + v + 16 * n) * BP + t0] = Br[n].get(v);
                     if (OUT)
-                        sh_C[k % 2][(ch + 16 * n) * BP + t] = T::load(Cr[e * S + n]);
+                        sh_C[k % 2][(ch + v + 16 * n) * BP + t0] = Cr[n].get(v);
                 }
             }
         };
         auto load_gate = [&](uint32_t k) {
-            if (OUT && z)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
-                    zr[e] = t < end ? z[t * a.d.z_step_stride] : raw(0);
-                }
+            if (!OUT)
+                return;
+            zr = four_channels(z.at);
+            z.go(!beyond(k) ? TT : to_next(k));
         };
         auto finish = [&](uint32_t k) {
-            if (OUT && on)
+            if (!OUT)
+                return;
+            float f[4];
+            Pack<T, 4> out;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int64_t t = start + (int64_t)k * TT + t0 + 16 * e;
-                    float v = sh_y[k % 3][ch * SP + t0 + 16 * e];
-                    if (z)
-                        v *= silu(T::load(zr[e]));
-                    if (t < end)
-                        y[t * a.d.y_step_stride] = T::store(v);
+            for (int v = 0; v < 4; ++v)
+                f[v] = sh_y[k % 3][(ch + v) * SP + t0];
+            if (a.z)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    f[v] *= silu(zr.get(v));
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                out.v[v] = T::store(f[v]);
+            if (start + (int64_t)k * TT + t0 < end) {
+                if (WHOLE) {
+                    store_pack<T, 4>(y, out);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (c + v < c_end)
+                            y[v] = out.v[v];
                 }
+            }
+            y += TT * a.d.y_step_stride;
         };
         if (tiles > 0) {
             load(0);
@@ -344,9 +408,13 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
         }
         if (tiles > 0)
             finish(tiles - 1);
-        if (OUT && on)
-            for (int64_t t = (end > start ? end : start) + t0; t < stop; t += 16)
-                y[t * a.d.y_step_stride] = T::store(0.0f);
+        raw *zeros = (raw *)a.y + b * a.d.y_batch_stride + c;
+        if (OUT)
+            for (int64_t t = (end > start ? end : start) + t0; t < stop; t += 64)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (WHOLE || c + v < c_end)
+                        zeros[t * a.d.y_step_stride + v] = T::store(0.0f);
         return;
     }
 
@@ -478,13 +546,12 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
 // or more and each has 128 steps or more (chains of loads start each span).
 static void spans_of(const rnn_scan_desc &d, Spans &sp)
 {
-    const int64_t tile = tile_steps(d.states <= 16 ? 1 : 2);
     sp.per = (uint32_t)(d.dim / d.groups);
     sp.per16 = (sp.per + 15) / 16;
     const int64_t groups16 = sp.per16 * d.groups;
     sp.groups16 = (uint32_t)groups16;
     sp.count = 1;
-    sp.length = (d.steps + tile - 1) / tile * tile;
+    sp.length = (d.steps + kTile - 1) / kTile * kTile;
     if (d.steps <= kFewSteps)
         return;
     int64_t count = 512 / (groups16 * d.batch);
@@ -492,7 +559,7 @@ static void spans_of(const rnn_scan_desc &d, Spans &sp)
         count = d.steps / 128;
     if (count < 4)
         return;
-    sp.length = ((d.steps + count - 1) / count + tile - 1) / tile * tile;
+    sp.length = ((d.steps + count - 1) / count + kTile - 1) / kTile * kTile;
     sp.count = (uint32_t)((d.steps + sp.length - 1) / sp.length);
 }
 
@@ -508,9 +575,9 @@ size_t scan_workspace(const rnn_scan_desc &d)
 template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp, hipStream_t s)
 {
     const dim3 grid((uint32_t)(sp.groups16 * sp.count * a.d.batch)), block(512);
-    const bool pad = a.d.states % 16 != 0;
+    const bool whole = a.d.states % 16 == 0 && sp.per % 16 == 0;
     if (sp.count > 1) {
-        if (pad)
+        if (whole)
             scan_kernel<T, S, true, false><<<grid, block, 0, s>>>(a, sp);
         else
             scan_kernel<T, S, false, false><<<grid, block, 0, s>>>(a, sp);
@@ -518,7 +585,7 @@ template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp,
         if (rc)
             return rc;
     }
-    if (pad)
+    if (whole)
         scan_kernel<T, S, true, true><<<grid, block, 0, s>>>(a, sp);
     else
         scan_kernel<T, S, false, true><<<grid, block, 0, s>>>(a, sp);
