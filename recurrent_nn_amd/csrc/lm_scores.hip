@@ -5,28 +5,32 @@
 //   logprob = (x_token - m) - log S,  entropy = log S - W / S   (for any m)
 //
 // Bound by HBM: the logits are read once.  What a thread keeps beside S and W
-// for its elements: the count that precedes the token, and the maxima of eight
-// parts of them.  The k-th largest of the threads' maxima is a bound that at
-// least k elements reach, so that only parts that reach it are read again (k of
-// them and a few, from the caches), and what they hold above it is ordered.
-// Few rows are cut into segments, which a second launch joins.
+// of its elements: the count that precedes the token, and the maxima of eight
+// parts of them.  From the threads' maxima each wave takes the value that
+// top / 4 of its lanes reach; the least of the four is a bound that at least
+// `top` elements reach, so that only the parts that reach it are read again
+// (a few more than `top`, from the caches), and what they hold above it is
+// ordered.  Few rows are cut into segments, which a second launch joins.
 #include "lm_common.h"
 
 namespace rnnamd {
 
 // The order of the entries: by value, larger first (NaN before all, -0 equal
 // to +0), then by index, lower first -- as one number, larger first, never 0.
-__device__ __forceinline__ uint64_t order_key(float v, uint32_t index)
+__device__ __forceinline__ uint32_t value_key(float v)
 {
-    uint32_t u = __float_as_uint(v + 0.0f);
-    u = v != v ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return ((uint64_t)u << 32) | (0xFFFFFFFFu - index);
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return v != v ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint64_t key)
+__device__ __forceinline__ float value_of(uint32_t u)
 {
-    const uint32_t u = (uint32_t)(key >> 32);
     return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
+__device__ __forceinline__ uint64_t order_key(float v, uint32_t index)
+{
+    return ((uint64_t)value_key(v) << 32) | (0xFFFFFFFFu - index);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
 
 constexpr float kLowest = -3.402823466e38f;
@@ -199,167 +203,210 @@ __device__ __forceinline__ void put_scores(const ScoresArgs &a, int64_t row, con
     }
 }
 
-// One segment of a row: packs [first, last) of 8 elements.
+// One segment of a row: packs [first, last) of 8 elements.  A thread takes
+// every 256th pack, U at a time: the loads of a batch are in flight while the
+// one before is summed.
 template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresArgs a,
                                                                       uint32_t segments,
                                                                       uint32_t segment_packs)
 {
     using raw = typename T::raw;
-    constexpr int PARTS = 8;
+    constexpr uint32_t PARTS = 8, U = sizeof(raw) == 2 ? 4 : 2, BATCH = 256 * U;
+    constexpr int WORDS = 8 * sizeof(raw) / 4;
     __shared__ uint64_t list[kList], sorted[RNN_SCORES_MAX_TOP];
-    __shared__ __attribute__((aligned(16))) float maxima[256];
-    __shared__ uint32_t count, items[256];
+    __shared__ float most[PARTS][256];
+    __shared__ uint32_t count, bounds[4];
+    __shared__ uint16_t items[256];
     __shared__ Part parts[4];
-    __shared__ float bound_value;
-    const uint32_t tid = threadIdx.x;
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t row = blockIdx.x / segments;
     const uint32_t segment = blockIdx.x % segments;
     const uint32_t V = (uint32_t)a.d.vocab, all = (V + 7) / 8;
     const uint32_t first = segment * segment_packs;
     const uint32_t last = first + segment_packs < all ? first + segment_packs : all;
+    const uint32_t whole = last < V / 8 ? last : V / 8;      // packs of all 8 elements end here
     const raw *x = (const raw *)a.logits + row * a.d.logits_stride;
+    const uint32_t batches = whole > first ? (whole - first + BATCH - 1) / BATCH : 0;
+    const uint32_t part_batches = (batches + PARTS - 1) / PARTS;
+
+    uint32_t next[U][WORDS];
+    auto load = [&](uint32_t batch) {           // beyond the end: the last pack again
+#pragma unroll
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t i = first + batch * BATCH + u * 256 + tid;
+            __builtin_memcpy(next[u], x + 8 * (int64_t)(i < whole ? i : whole - 1), sizeof(next[u]));
+        }
+    };
+    if (batches > 0)
+        load(0);
+
     const Token tk = token_of<T>(a, row, x);
     const float mine = tk.value;
+    // What counts as before the token: in packs before the token's own
+    // !(x <= lower), lower the next value below it; from its own on
+    // !(x <= mine).  The own pack's equal entries before it are added after.
+    // (-inf is preceded by everything of lower index; a NaN is counted below.)
     const bool unordered = mine != mine;
-
-    // What counts as before the token: packs before the token's own by
-    // !(x <= lower), lower the next value below it; packs from its own on by
-    // !(x <= mine).  Its own pack's equal entries before it are added below.
-    // (A NaN is preceded by the NaN of lower index only; -inf by all of them.)
     const uint32_t token_pack = tk.known ? (uint32_t)(tk.id / 8) : 0;
-    float lower, upper = unordered ? __builtin_inff() : mine;
+    float lower = mine;
     {
         const uint32_t u = __float_as_uint(mine);
         lower = mine == 0.0f ? -__uint_as_float(1u)
                              : __uint_as_float((u & 0x80000000u) ? u + 1u : u - 1u);
-        if (unordered)
-            lower = __builtin_inff();
-        else if (mine == -__builtin_inff())
+        if (mine == -__builtin_inff())
             lower = __uint_as_float(0x7FC00000u);
     }
-    const uint32_t upper_counts = unordered ? 0u : ~0u;
 
     Part p{{kLowest, 0.0f, 0.0f}, 0};
-    float most[PARTS];
-    const uint32_t mine_packs = last > first + tid ? (last - first - tid + 255) / 256 : 0;
-    const uint32_t part_packs = ((last - first + 255) / 256 + PARTS - 1) / PARTS;
-    auto one = [&](const Pack<T, 8> &pk, uint32_t i, float &top_of_part) {
-        float f[8];
-#pragma unroll
-        for (int v = 0; v < 8; ++v)
-            f[v] = T::load(pk.v[v]);
+    uint32_t before = 0;                        // of the wave
+    float top_of_part = -__builtin_inff(), top_of_all = top_of_part;
+    auto one = [&](const float (&f)[8], uint32_t i) {
         const float pm = __builtin_fmaxf(
             __builtin_fmaxf(__builtin_fmaxf(f[0], f[1]), __builtin_fmaxf(f[2], f[3])),
             __builtin_fmaxf(__builtin_fmaxf(f[4], f[5]), __builtin_fmaxf(f[6], f[7])));
         top_of_part = __builtin_fmaxf(top_of_part, pm);
-        if (pm > p.s.m + 8.0f)          // rare after the first pack
+        if (pm > p.s.m + 8.0f)                  // rare after the first pack
             p.s.rebase(pm);
-        const bool below = i < token_pack;
-        const float edge = below ? lower : upper;
-        uint32_t n = 0;
+        const float edge = i < token_pack ? lower : mine;
         float e[8];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
             const float d = f[v] - p.s.m;
             e[v] = __builtin_amdgcn_exp2f(d * kLog2e);
             p.s.cross = __builtin_fmaf(e[v], __builtin_fmaxf(d, kFar), p.s.cross);
-            n += !(f[v] <= edge);
+            before += __popcll(__ballot(!(f[v] <= edge)));
         }
         p.s.sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        p.before += n & (below ? ~0u : upper_counts);
     };
+    for (uint32_t b = 0, in_part = 0, part = 0; b < batches; ++b) {
+        uint32_t now[U][WORDS];
 #pragma unroll
-    for (int s = 0; s < PARTS; ++s) {
-        most[s] = -__builtin_inff();
-        const uint32_t from = s * part_packs;
-        const uint32_t to = from + part_packs < mine_packs ? from + part_packs : mine_packs;
-        uint32_t j = from;
-        for (; j + 4 <= to; j += 4) {
-            Pack<T, 8> pk[4];
+        for (uint32_t u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                pk[u] = logits_pack<T>(x, first + tid + 256 * (j + u), V);
+            for (int w = 0; w < WORDS; ++w)
+                now[u][w] = next[u][w];
+        if (b + 1 < batches)
+            load(b + 1);
+        const bool end = b + 1 == batches;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                one(pk[u], first + tid + 256 * (j + u), most[s]);
+        for (uint32_t u = 0; u < U; ++u) {
+            const uint32_t i = first + b * BATCH + u * 256 + tid;
+            const bool beyond = end && i >= whole;
+            float f[8];
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                if constexpr (sizeof(raw) == 4)
+                    f[v] = T::load(now[u][v]);
+                else
+                    f[v] = T::load((raw)(v % 2 ? now[u][v / 2] >> 16 : now[u][v / 2] & 0xFFFFu));
+            }
+            if (end) {
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    f[v] = beyond ? -__builtin_inff() : f[v];
+                // (they must not count as before a token)
+                one(f, beyond ? ~0u : i);
+            } else {
+                one(f, i);
+            }
         }
-        for (; j < to; ++j)
-            one(logits_pack<T>(x, first + tid + 256 * j, V), first + tid + 256 * j, most[s]);
+        if (++in_part == part_batches || end) {
+            most[part][tid] = top_of_part;
+            top_of_all = __builtin_fmaxf(top_of_all, top_of_part);
+            top_of_part = -__builtin_inff();
+            in_part = 0;
+            ++part;
+            if (end)
+                for (; part < PARTS; ++part)
+                    most[part][tid] = -__builtin_inff();
+        }
     }
-    if (tid == 0 && tk.known && token_pack >= first && token_pack < last)
-        for (uint32_t v = token_pack * 8; v < (uint32_t)tk.id; ++v) {
-            const float f = T::load(x[v]);
-            p.before += f == mine || (unordered && f != f);
-        }
-
-    // over the workgroup
-    float mx = most[0];
+    // the last elements, fewer than a pack, one a thread
+    const uint32_t rest = last * 8 > V ? V - whole * 8 : 0;
+    const float f_rest = tid < rest ? T::load(x[whole * 8 + tid]) : -__builtin_inff();
+    if (wave == 0 && rest > 0) {
+        float f[8];
 #pragma unroll
-    for (int s = 1; s < PARTS; ++s)
-        mx = __builtin_fmaxf(mx, most[s]);
-    maxima[tid] = mx;
+        for (int v = 1; v < 8; ++v)
+            f[v] = -__builtin_inff();
+        f[0] = f_rest;
+        one(f, ~0u);
+        top_of_all = __builtin_fmaxf(top_of_all, f_rest);
+    }
+    if (lane == 0)
+        p.before = before;
+    if (tid == 0 && tk.known && token_pack >= first && token_pack < last)
+        for (uint32_t v = token_pack * 8; v < (uint32_t)tk.id; ++v)
+            p.before += T::load(x[v]) == mine;
     p = over_workgroup(p, parts);
+    const bool odd = !(p.s.sum < __builtin_inff());     // NaN or infinite entries
+    if (tk.known && (odd || unordered)) {               // count by the keys themselves
+        const uint64_t mine_key = order_key(mine, (uint32_t)tk.id);
+        Part q{{kLowest, 0.0f, 0.0f}, 0};
+        for (uint32_t v = first * 8 + tid; v < V && v < last * 8; v += 256)
+            q.before += order_key(T::load(x[v]), v) > mine_key;
+        __syncthreads();
+        p.before = over_workgroup(q, parts).before;
+    }
 
     const int top = a.d.top;
     Best best;
     best.begin(list, sorted, &count, top);
     if (top > 0) {
-        // the bound: the top-th of the threads' maxima, ties in any order
-        uint32_t place = 0;
-        for (int j = 0; j < 256; j += 4) {
-            const float4 o = *(const float4 *)&maxima[j];
-            place += o.x > mx || (o.x == mx && j + 0 < (int)tid);
-            place += o.y > mx || (o.y == mx && j + 1 < (int)tid);
-            place += o.z > mx || (o.z == mx && j + 2 < (int)tid);
-            place += o.w > mx || (o.w == mx && j + 3 < (int)tid);
-        }
-        if (place == (uint32_t)top - 1)
-            bound_value = mx;
+        // The bound, to 24 bits: the largest t that enough lanes reach.
+        const uint32_t key = value_key(top_of_all), enough = (top + 3) / 4;
+        uint32_t t = 0;
+        for (uint32_t bit = 1u << 31; bit >= 1u << 8; bit /= 2)
+            if (__popcll(__ballot(key >= (t | bit))) >= (int)enough)
+                t |= bit;
+        if (lane == 0)
+            bounds[wave] = t;
         __syncthreads();
-        // (m may exceed no element: NaN and infinities show in the sum)
-        const bool odd = !(p.s.sum < __builtin_inff());
-        const float edge = bound_value;
 #pragma unroll
-        for (int s = 0; s < PARTS; ++s)
-            if (!odd && most[s] >= edge) {
-                const uint32_t at = atomicAdd(&count, 1u);
-                if (at < 256)
-                    items[at] = s * 256 + tid;
-            }
+        for (int i = 0; i < 4; ++i)
+            t = bounds[i] < t ? bounds[i] : t;
+        // (cut to 24 bits, -inf lies below every number's key)
+        const float edge = t < value_key(kLowest) ? -__builtin_inff() : value_of(t);
+        if (!odd && batches > 0)
+            for (uint32_t s = 0; s < PARTS; ++s)
+                if (most[s][tid] >= edge) {
+                    const uint32_t at = atomicAdd(&count, 1u);
+                    if (at < 256)
+                        items[at] = (uint16_t)(s * 256 + tid);
+                }
         uint32_t n = best.offered();
         best.forget();
         const bool few = !odd && n <= 256;
-        const uint32_t packs = few ? n * part_packs : last - first;
-        auto offer = [&](const Pack<T, 8> &pk, uint32_t i, bool on, int v) {
-            const float f = T::load(pk.v[v]);
-            best.offer(order_key(f, 8 * i + v),
-                       on && 8 * i + v < V && (odd || f >= edge));
-        };
+        const uint32_t item_packs = part_batches * U;
+        const uint32_t packs = few ? n * item_packs : last - first;
+        auto wanted = [&](float f) { return odd || f >= edge; };
+        if (few)
+            best.offer(order_key(f_rest, whole * 8 + tid), tid < rest && wanted(f_rest));
         for (uint32_t base = 0; base < packs; base += 256) {
             const uint32_t q = base + tid;
             bool on = q < packs;
             uint32_t i = first + q;
             if (few && on) {
-                const uint32_t item = items[q / part_packs];
-                const uint32_t j = item / 256 * part_packs + q % part_packs;
-                i = first + item % 256 + 256 * j;
-                on = i < last;
+                const uint32_t item = items[q / item_packs], r = q % item_packs;
+                i = first + item / 256 * part_batches * BATCH + r * 256 + item % 256;
+                on = i < whole;
             }
             Pack<T, 8> pk{};
             if (on)
                 pk = logits_pack<T>(x, i, V);
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-                offer(pk, i, on, v);
+            for (int v = 0; v < 8; ++v) {
+                const float f = T::load(pk.v[v]);
+                best.offer(order_key(f, 8 * i + v), on && 8 * i + v < V && wanted(f));
+            }
             n = best.offered();
             if (n > kList) {            // too many at once: an eighth of them at a time
                 best.forget();
 #pragma unroll 1
                 for (int v = 0; v < 8; ++v) {
-                    const uint64_t key = order_key(T::load(pk.v[0]), 8 * i + v);
-                    best.offer(key, on && 8 * i + v < V && (odd || T::load(pk.v[0]) >= edge));
-                    n = best.offered();
-                    best.order(n);
+                    const float f = T::load(pk.v[0]);
+                    best.offer(order_key(f, 8 * i + v), on && 8 * i + v < V && wanted(f));
+                    best.order(best.offered());
 #pragma unroll
                     for (int u = 0; u < 7; ++u)
                         pk.v[u] = pk.v[u + 1];
@@ -368,8 +415,7 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
                 best.order(n);
             }
         }
-        n = best.offered();
-        best.order(n);
+        best.order(best.offered());
     }
     if (segments == 1) {
         put_scores(a, row, p, tk, sorted, best.kept);
@@ -416,14 +462,14 @@ template <class T> __global__ __launch_bounds__(256) void scores_join_kernel(Sco
     put_scores(a, row, p, tk, sorted, best.kept);
 }
 
-// Segments of a row: as many as bring about 512 workgroups, of 4096 elements
+// Segments of a row: as many as bring about 512 workgroups, of 8192 elements
 // or more each.
 static uint32_t segments_of(const rnn_scores_desc &d, uint32_t &packs)
 {
     const int64_t all = (d.vocab + 7) / 8;
     int64_t n = 512 / d.rows;
-    if (n > (all + 511) / 512)
-        n = (all + 511) / 512;
+    if (n > (all + 1023) / 1024)
+        n = (all + 1023) / 1024;
     if (n < 1)
         n = 1;
     packs = (uint32_t)((all + n - 1) / n);

@@ -335,14 +335,15 @@ def token_scores(logits, tokens=None, top: int = 0, stream=None) -> TokenScores:
     _, desc, size, rows = known
 
     def call(s):
-        # one allocation for all the outputs of a row
-        f = logits.new_empty((2 + top) * rows, dtype=torch.float32)
-        i = logits.new_empty((1 + top) * rows, dtype=torch.int32)
         ws = logits.new_empty((size + 3) // 4, dtype=torch.float32) if size else None
-        lp, en, tl = f[:rows], f[rows:2 * rows], f[2 * rows:].view(rows, top)
-        rk, ti = i[:rows], i[rows:].view(rows, top)
+        lp, en = logits.new_empty((2, rows), dtype=torch.float32).unbind(0)
+        tl = logits.new_empty((rows, top), dtype=torch.float32)
+        ti = logits.new_empty((rows, top), dtype=torch.int32)
+        rk = None
         if tokens is None:
-            lp = rk = None
+            lp = None
+        else:
+            rk = ti.new_empty(rows)
         _check(lib.rnn_token_scores(desc, s, _ptr(ws), size, logits.data_ptr(), _ptr(tokens),
                                     _ptr(lp), en.data_ptr(), _ptr(rk), tl.data_ptr(),
                                     ti.data_ptr()), "rnn_token_scores")
