@@ -6,6 +6,7 @@
 // loads, 32x32x32 products, the scales in the epilogue.  Few rows: bound by
 // reading w once; it goes from memory to the matrix unit's registers.
 #include <type_traits>
+#include <utility>
 
 #include "lm_common.h"
 
@@ -25,12 +26,14 @@ struct ProjectGo {
 
 // ---------------------------------------------------------------------------
 // Many rows.  A workgroup has BM tokens x BN outputs, WM x WN waves.  A step
-// is 128 columns: a tile row is 128 bytes of LDS, all banks once; its 16-byte
-// pieces are permuted by the row (piece p of row r holds columns 16 (p xor r%8)
-// on) so that the eight rows that one pass of a 16-byte read takes are in
-// different banks.  The permutation is applied to the addresses that the
-// direct loads read from: in LDS they write in order.  Two buffers; a step's
-// loads are in flight during the products of the one before.
+// is 64 columns: a tile row is 64 bytes of LDS, whose 16-byte pieces are
+// permuted by the row (piece p of row r holds columns 16 (p xor r/4%4) on), so
+// that the sixteen rows that one pass of a 16-byte read takes (lanes 0-3, 12-15,
+// 20-23, 24-27, then the others) are in different banks.  The permutation is applied to the addresses that the direct loads
+// read from: in LDS they write in order.  Four buffers: three steps' loads are
+// in flight during the products of one, and a wave waits for its own part of
+// the next step only (by count), then for the others at the step's one barrier.
+// Operands are read half a step ahead, between the products of the half before.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void load_to_lds(const int8_t *p, int8_t *lds)
@@ -39,17 +42,37 @@ __device__ __forceinline__ void load_to_lds(const int8_t *p, int8_t *lds)
                                      (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
 }
 
-template <class T, int BM, int BN, int WM, int WN>
+// Until at most N of the wave's loads are out (they come in order), and none
+// of its reads of LDS.
+template <int N> __device__ __forceinline__ void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+// READS reads of LDS (a later half's operands) and LOADS loads (a later step's)
+// spread between the products I...: a product takes 4 cycles to issue and runs
+// for 32.
+template <int READS, int LOADS, int... I>
+__device__ __forceinline__ void interleave(std::integer_sequence<int, I...>)
+{
+    constexpr int N = sizeof...(I);
+    ((__builtin_amdgcn_sched_group_barrier(0x008, 1, 0),
+      __builtin_amdgcn_sched_group_barrier(0x100, READS * (I + 1) / N - READS * I / N, 0),
+      __builtin_amdgcn_sched_group_barrier(0x020, LOADS * (I + 1) / N - LOADS * I / N, 0)),
+     ...);
+}
+
+template <class T, int BM, int BN, int WM, int WN, int BUFFERS>
 __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g, uint32_t m_tiles,
                                                                     uint32_t n_tiles)
 {
     using raw = typename T::raw;
-    constexpr int THREADS = 64 * WM * WN, KB = 128;
+    constexpr int THREADS = 64 * WM * WN, KB = 64;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;       // 32 x 32 tiles of a wave
-    constexpr int XP = BM * 8 / THREADS, WP = BN * 8 / THREADS;   // pieces a thread loads
+    constexpr int XP = BM * 4 / THREADS, WP = BN * 4 / THREADS;   // pieces a thread loads
     constexpr int ON = TN * 32, OP = ON + 4;                  // epilogue: a row of a wave's outputs
-    static_assert(WM * WN * 32 * OP * 4 <= 2 * (BM + BN) * KB, "epilogue fits the tiles' memory");
-    __shared__ __attribute__((aligned(128))) int8_t lds[2 * (BM + BN) * KB];
+    static_assert(WM * WN * 32 * OP * 4 <= BUFFERS * (BM + BN) * KB, "epilogue fits the tiles' memory");
+    __shared__ __attribute__((aligned(128))) int8_t lds[BUFFERS * (BM + BN) * KB];
 
     // Tiles in bands of 8 tiles of tokens, each XCD (workgroups go to them in
     // turn) a run of adjacent ones: what runs at a time on an XCD shares rows of
@@ -68,38 +91,46 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
     int kx[XP], kw[WP];
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
-        const int q = i * THREADS + tid, r = q / 8;
+        const int q = i * THREADS + tid, r = q / 4;
         const int row = row0 + r < g.rows ? row0 + r : g.rows - 1;
-        kx[i] = (q % 8 ^ (r & 7)) * 16;
+        kx[i] = (q % 4 ^ (r / 4 & 3)) * 16;
         xp[i] = g.x + (int64_t)row * g.x_stride + kx[i];
     }
 #pragma unroll
     for (int i = 0; i < WP; ++i) {
-        const int q = i * THREADS + tid, r = q / 8;
+        const int q = i * THREADS + tid, r = q / 4;
         const int row = out0 + r < g.outs ? out0 + r : g.outs - 1;
-        kw[i] = (q % 8 ^ (r & 7)) * 16;
+        kw[i] = (q % 4 ^ (r / 4 & 3)) * 16;
         wp[i] = g.w + (int64_t)row * g.w_stride + kw[i];
     }
-    auto stage = [&](int buf, int k0) {
-        int8_t *X = lds + buf * (BM + BN) * KB, *W = X + BM * KB;
-        if (k0 + KB <= g.k_end) {
+    auto stage = [&](int k) {
+        int8_t *X = lds + k % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
 #pragma unroll
-            for (int i = 0; i < XP; ++i)
-                load_to_lds(xp[i] + k0, X + (i * THREADS + wave * 64) * 16);
+        for (int i = 0; i < XP; ++i)
+            load_to_lds(xp[i] + k * KB, X + (i * THREADS + wave * 64) * 16);
 #pragma unroll
-            for (int i = 0; i < WP; ++i)
-                load_to_lds(wp[i] + k0, W + (i * THREADS + wave * 64) * 16);
-        } else {                        // the last columns: zeros behind them
-#pragma unroll
-            for (int i = 0; i < XP; ++i)
-                *(v4i *)(X + (i * THREADS + tid) * 16) =
-                    k0 + kx[i] < g.k_end ? *(const v4i *)(xp[i] + k0) : v4i{};
-#pragma unroll
-            for (int i = 0; i < WP; ++i)
-                *(v4i *)(W + (i * THREADS + tid) * 16) =
-                    k0 + kw[i] < g.k_end ? *(const v4i *)(wp[i] + k0) : v4i{};
-        }
+        for (int i = 0; i < WP; ++i)
+            load_to_lds(wp[i] + k * KB, W + (i * THREADS + wave * 64) * 16);
     };
+
+    // the scales of the epilogue's rows and columns, on their way from the start
+    constexpr int PASSES = 32 / (64 / (ON / 8));
+    const int o = out0 + wn * ON + lane % (ON / 8) * 8;
+    float ws[8], bs[8] = {}, xs[TM][PASSES];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        const int col = o + v < g.outs ? o + v : g.outs - 1;
+        ws[v] = g.w_scale[col];
+        if (g.bias)
+            bs[v] = g.bias[col];
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int row = row0 + (wm * TM + m) * 32 + lane / (ON / 8) + i * (64 / (ON / 8));
+            xs[m][i] = g.x_scale[row < g.rows ? row : g.rows - 1];
+        }
 
     v16i acc[TN][TM];
 #pragma unroll
@@ -107,47 +138,98 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
 #pragma unroll
         for (int m = 0; m < TM; ++m)
             acc[n][m] = v16i{};
-
-    const int steps = (g.k_end + KB - 1) / KB;
-    if (steps > 0)
-        stage(0, 0);
-    __syncthreads();
-    for (int k = 0; k < steps; ++k) {
-        if (k + 1 < steps)
-            stage((k + 1) % 2, (k + 1) * KB);
-        const int8_t *X = lds + k % 2 * (BM + BN) * KB, *W = X + BM * KB;
-        X += (wm * TM * 32 + lane % 32) * KB;
-        W += (wn * TN * 32 + lane % 32) * KB;
+    // Operands of half a step (32 columns), and the products of them.
+    struct Half {
+        v4i x[TM], w[TN];
+    };
+    auto fetch = [&](int k, int half, Half &f) {
+        const int8_t *X = lds + k % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
+        const int at = ((half * 2 + lane / 32) ^ (lane / 4 & 3)) * 16;
+        X += (wm * TM * 32 + lane % 32) * KB + at;
+        W += (wn * TN * 32 + lane % 32) * KB + at;
 #pragma unroll
-        for (int kk = 0; kk < KB / 32; ++kk) {
-            const int at = ((kk * 2 + lane / 32) ^ (lane & 7)) * 16;
-            v4i fx[TM], fw[TN];
+        for (int m = 0; m < TM; ++m)
+            f.x[m] = *(const v4i *)(X + m * 32 * KB);
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
+            f.w[n] = *(const v4i *)(W + n * 32 * KB);
+    };
+    auto products = [&](const Half &f) {
+#pragma unroll
+        for (int n = 0; n < TN; ++n)
 #pragma unroll
             for (int m = 0; m < TM; ++m)
-                fx[m] = *(const v4i *)(X + m * 32 * KB + at);
+                acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[n], f.x[m], acc[n][m], 0, 0, 0);
+    };
+    using Products = std::make_integer_sequence<int, TM * TN>;
+
+    const int steps = g.k_end / KB;             // whole ones
 #pragma unroll
-            for (int n = 0; n < TN; ++n)
-                fw[n] = *(const v4i *)(W + n * 32 * KB + at);
-#pragma unroll
-            for (int n = 0; n < TN; ++n)
-#pragma unroll
-                for (int m = 0; m < TM; ++m)
-                    acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[n], fx[m], acc[n][m], 0, 0, 0);
-        }
-        __syncthreads();
+    for (int k = 0; k < BUFFERS; ++k)
+        if (k < steps)
+            stage(k);
+    // Step k's loads have come for all waves: those of the BUFFERS - 2 steps after
+    // may be out.  The barrier also says that all have read step k - 1, whose
+    // buffer step k + BUFFERS - 1 gets.
+    auto step = [&](int k, Half &even, Half &odd, auto more) {
+        constexpr bool MORE = decltype(more)::value;
+        fetch(k, 1, odd);
+        products(even);
+        interleave<TM + TN, 0>(Products{});
+        wait_loads<MORE ? (BUFFERS - 2) * (XP + WP) : 0>();
+        __builtin_amdgcn_s_barrier();
+        if (MORE)
+            stage(k + BUFFERS);
+        fetch(k + 1, 0, even);
+        products(odd);
+        if (MORE)
+            interleave<TM + TN, XP + WP>(Products{});
+        else
+            interleave<TM + TN, 0>(Products{});
+    };
+    if (steps > 0) {
+        Half even, odd;
+        if (steps >= BUFFERS)
+            wait_loads<(BUFFERS - 1) * (XP + WP)>();
+        else
+            wait_loads<0>();
+        __builtin_amdgcn_s_barrier();
+        fetch(0, 0, even);
+        int k = 0;
+        for (; k + BUFFERS < steps; ++k)
+            step(k, even, odd, std::true_type{});
+        for (; k + 1 < steps; ++k)
+            step(k, even, odd, std::false_type{});
+        fetch(steps - 1, 1, odd);
+        products(even);
+        products(odd);
     }
+    if (g.k_end % KB) {                         // the last columns, zeros behind them
+        const int k0 = steps * KB;
+        int8_t *X = lds + steps % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < XP; ++i)
+            *(v4i *)(X + (i * THREADS + tid) * 16) =
+                k0 + kx[i] < g.k_end ? *(const v4i *)(xp[i] + k0) : v4i{};
+#pragma unroll
+        for (int i = 0; i < WP; ++i)
+            *(v4i *)(W + (i * THREADS + tid) * 16) =
+                k0 + kw[i] < g.k_end ? *(const v4i *)(wp[i] + k0) : v4i{};
+        __syncthreads();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            Half f;
+            fetch(steps, half, f);
+            products(f);
+        }
+    }
+    __syncthreads();
 
     // Epilogue.  A lane holds groups of four outputs of one token; through LDS
     // (each wave its own part) it gets eight adjacent outputs of a token and
     // stores them as one piece of a row.
     int *tile = (int *)lds + wave * 32 * OP;
-    const int o = out0 + wn * ON + lane % (ON / 8) * 8;
-    float ws[8], bs[8];
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-        ws[v] = o + v < g.outs ? g.w_scale[o + v] : 0.0f;
-        bs[v] = g.bias && o + v < g.outs ? g.bias[o + v] : 0.0f;
-    }
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
 #pragma unroll
@@ -159,17 +241,17 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
         __builtin_amdgcn_wave_barrier();
         const int t0 = row0 + (wm * TM + m) * 32;
 #pragma unroll
-        for (int r = lane / (ON / 8); r < 32; r += 64 / (ON / 8)) {
+        for (int i = 0; i < PASSES; ++i) {
+            const int r = lane / (ON / 8) + i * (64 / (ON / 8));
             const v4i *from = (const v4i *)(tile + r * OP + lane % (ON / 8) * 8);
             const v4i lo = from[0], hi = from[1];
             const int row = t0 + r;
             if (row >= g.rows)
                 continue;
-            const float xs = g.x_scale[row];
             Pack<T, 8> out;
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
-                float f = (float)(v < 4 ? lo[v % 4] : hi[v % 4]) * (xs * ws[v]);
+                float f = (float)(v < 4 ? lo[v % 4] : hi[v % 4]) * (xs[m][i] * ws[v]);
                 if (g.bias)
                     f += bs[v];
                 out.v[v] = T::store(f);
@@ -354,12 +436,12 @@ size_t project_workspace(const rnn_quant_desc &d)
     return up256((size_t)d.rows * pitch(d.cols)) + up256((size_t)d.rows * 4);
 }
 
-template <class T, int BM, int BN, int WM, int WN>
+template <class T, int BM, int BN, int WM, int WN, int BUFFERS>
 static void tiles_go(const ProjectGo &g, hipStream_t s)
 {
     const uint32_t m = (uint32_t)((g.rows + (int64_t)BM - 1) / BM);
     const uint32_t n = (uint32_t)((g.outs + (int64_t)BN - 1) / BN);
-    project_tiles_kernel<T, BM, BN, WM, WN><<<dim3(m * n), dim3(64 * WM * WN), 0, s>>>(g, m, n);
+    project_tiles_kernel<T, BM, BN, WM, WN, BUFFERS><<<dim3(m * n), dim3(64 * WM * WN), 0, s>>>(g, m, n);
 }
 
 template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &a, hipStream_t s)
@@ -397,11 +479,11 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
     if (tiles(64, 64) > 0x7fffffff)
         return (int)hipErrorInvalidConfiguration;
     if (tiles(256, 256) >= 192)
-        tiles_go<T, 256, 256, 2, 4>(g, s);
+        tiles_go<T, 256, 256, 2, 4, 4>(g, s);
     else if (tiles(128, 128) >= 192)
-        tiles_go<T, 128, 128, 2, 2>(g, s);
+        tiles_go<T, 128, 128, 2, 2, 4>(g, s);
     else
-        tiles_go<T, 64, 64, 2, 2>(g, s);
+        tiles_go<T, 64, 64, 2, 2, 4>(g, s);
     return (int)hipGetLastError();
 }
 
