@@ -8,6 +8,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/recurrent_nn_amd.h"
 
@@ -109,16 +110,22 @@ __device__ __forceinline__ RowScale row_scale(float most, bool finite)
     return {127.0f / most, most / 127.0f};
 }
 
-// The largest magnitude over a wave, as bits: magnitudes order as their bits
-// do, infinities and NaN above all finite ones.
+// The largest of a wave's values, in all lanes.  (Magnitudes order as their bits
+// do, infinities and NaN above all finite ones.)
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int m = 32; m > 0; m /= 2) {
-        const uint32_t o = __shfl_xor(v, m, 64);
+    auto with = [&](auto ctrl, auto rows) {     // what has no lane to come from is 0
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
+            0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
         v = o > v ? o : v;
-    }
-    return v;
+    };
+    with(std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});    // lane xor 1
+    with(std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});    // lane xor 2
+    with(std::integral_constant<int, 0x141>{}, std::integral_constant<int, 0xF>{});   // half mirror
+    with(std::integral_constant<int, 0x140>{}, std::integral_constant<int, 0xF>{});   // row mirror
+    with(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row 0 to 1, 2 to 3
+    with(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // rows 0, 1 to 2, 3
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 constexpr uint32_t kInfBits = 0x7F800000u;
 

@@ -271,151 +271,174 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (up to 64, in tiles of 16).  A workgroup has 16 outputs; its four
-// waves take steps of 128 columns in turn and add their sums in LDS.  A lane
-// loads 32 bytes of a weight row, a row's 128 bytes by four lanes, straight
-// into the operands of 16x16x64 products.  With FROM (the rows' type) x is
-// rounded in the call: each workgroup does it for itself, into LDS, while its
-// first weights are on their way; that is less than a launch for few
-// elements.
+// Few rows (up to 16, and at least a column).  A workgroup has 16 outputs; its four waves take steps
+// of 128 columns in turn and add their sums in LDS.  A load takes 64 bytes of
+// 16 weight rows, straight into the operands of 16x16x64 products; four steps
+// of both sides are in flight.  With FROM (the rows' type) x is rounded in the
+// call: each workgroup does it for itself, into LDS, while its first weights
+// are on their way; that is less than a launch for few elements.
 // ---------------------------------------------------------------------------
 
-constexpr int kFusedElements = 16384;      // most elements of x for that
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 16;
+constexpr int kFusedElements = 16384;      // most elements of x to round inside
 
 struct NoSource {};
 
-template <class T, class FROM, int TILES>
+template <class T, class FROM>
 __global__ __launch_bounds__(256) void project_rows_kernel(ProjectGo g, const void *x_source,
                                                           int64_t source_stride, int32_t cols)
 {
     constexpr bool FUSED = !std::is_same<FROM, NoSource>::value;
-    constexpr int AHEAD = 4;                     // steps of weights in flight
+    constexpr int AHEAD = 4;                     // steps in flight
     extern __shared__ __attribute__((aligned(16))) int8_t q_lds[];   // FUSED: rows of pitch, then scales
-    __shared__ __attribute__((aligned(16))) int sums[3][TILES][256];
-    __shared__ uint32_t row_max[4][FUSED ? 16 : 1];
+    __shared__ __attribute__((aligned(16))) int sums[3][256];
+    __shared__ uint32_t row_max[16];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     const int out0 = blockIdx.x * 16;
-    const int wrow = out0 + lane % 16 < g.outs ? out0 + lane % 16 : g.outs - 1;
-    const int8_t *w = g.w + (int64_t)wrow * g.w_stride;
-    const int k_lane = lane / 16 * 32;
     const int steps = (g.k_end + 127) / 128;
-
-    auto piece = [&](const int8_t *p, int k) { return k < g.k_end ? *(const v4i *)(p + k) : v4i{}; };
-    v4i wf[AHEAD][2];
-    auto fetch = [&](int step, v4i (&f)[2]) {
-        const int k = step * 128 + k_lane;
-        f[0] = piece(w, k);
-        f[1] = piece(w, k + 16);
-    };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        fetch(wave + 4 * i, wf[i]);
-
     const int pitch = steps * 128 + 16;
     float *q_scale = (float *)(q_lds + g.rows * pitch);
+
+    // a thread's packs of 8 elements of x, 256 apart, row after row
+    constexpr int KEEP = FUSED ? kFusedElements / 8 / 256 : 1;
+    const int row_packs = steps * 16;
+    typedef typename std::conditional<FUSED, FROM, BF16>::type X;
+    Pack<X, 8> keep[KEEP];
+    auto row_of = [&](int j) { return ((int)threadIdx.x + 256 * j) / row_packs; };
     if constexpr (FUSED) {
-        using raw = typename FROM::raw;
-        const int packs = steps * 16;            // of 8 elements, zeros past cols
-        auto pack = [&](int r, int i) {
-            const raw *x = (const raw *)x_source + r * source_stride + 8 * i;
-            Pack<FROM, 8> p{};
-            if (8 * i + 8 <= cols) {
-                p = load_pack<FROM, 8>(x);
-            } else {
+        if (threadIdx.x < 16)
+            row_max[threadIdx.x] = 0;
 #pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    if (8 * i + v < cols)
-                        p.v[v] = x[v];
+        for (int j = 0; j < KEEP; ++j) {
+            const int r = row_of(j), k = ((int)threadIdx.x + 256 * j - r * row_packs) * 8;
+            const typename X::raw *x = (const typename X::raw *)x_source + r * source_stride + k;
+            keep[j] = Pack<X, 8>{};
+            if (r < g.rows) {
+                if (k + 8 <= cols) {
+                    keep[j] = load_pack<X, 8>(x);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        if (k + v < cols)
+                            keep[j].v[v] = x[v];
+                }
             }
-            return p;
-        };
-#pragma unroll 4
-        for (int r = 0; r < g.rows; ++r) {
-            uint32_t most = 0;
-            for (int i = threadIdx.x; i < packs; i += 256)
-                most = pack_max<FROM, 8>(pack(r, i), most);
-            most = wave_max(most);
-            if (lane == 0)
-                row_max[wave][r] = most;
+        }
+    }
+
+    const int wrow = out0 + lane % 16 < g.outs ? out0 + lane % 16 : g.outs - 1;
+    const int xrow = lane % 16 < g.rows ? lane % 16 : g.rows - 1;
+    const int8_t *w = g.w + (int64_t)wrow * g.w_stride;
+    const int8_t *x = FUSED ? q_lds + xrow * pitch : g.x + (int64_t)xrow * g.x_stride;
+    // Past the last columns the last ones are loaded again (no load depends on a
+    // condition: it would be waited for on the spot); x is zero there.
+    auto piece = [&](const int8_t *p, int k) {
+        return *(const v4i *)(p + (k < g.k_end ? k : g.k_end - 16));
+    };
+    struct Group {                      // AHEAD steps of the wave, from its step `s`
+        v4i w[AHEAD][2], x[AHEAD][2];
+    };
+    auto fetch = [&](int s, Group &f) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (s + 4 * i) * 128 + lane / 16 * 16 + 64 * h;
+                f.w[i][h] = piece(w, k);
+                if (!FUSED)
+                    f.x[i][h] = piece(x, k);
+            }
+    };
+    Group first, second;
+    fetch(wave, first);
+
+    if constexpr (FUSED) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j) {
+            const int r = row_of(j);
+            uint32_t most = pack_max<X, 8>(keep[j], 0);
+            if (256 * j >= g.rows * row_packs)
+                break;
+            // one addition to LDS for a wave that is in one row
+            if (__builtin_amdgcn_readfirstlane(r) == __builtin_amdgcn_readlane(r, 63)) {
+                most = wave_max(most);
+                if (lane == 0 && r < g.rows)
+                    atomicMax(&row_max[r], most);
+            } else if (r < g.rows) {
+                atomicMax(&row_max[r], most);
+            }
         }
         __syncthreads();
-        for (int r = 0; r < g.rows; ++r) {
-            uint32_t most = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                most = row_max[i][r] > most ? row_max[i][r] : most;
+        for (int j = 0; j < KEEP; ++j) {
+            const int r = row_of(j), k = ((int)threadIdx.x + 256 * j - r * row_packs) * 8;
+            if (r >= g.rows)
+                break;
+            const uint32_t most = row_max[r];
             const RowScale rs = row_scale(__uint_as_float(most), most < kInfBits);
-            for (int i = threadIdx.x; i < packs; i += 256)
-                *(uint2 *)(q_lds + r * pitch + 8 * i) = pack_8bit<FROM>(pack(r, i), rs.factor);
-            if (threadIdx.x == 0)
+            *(uint2 *)(q_lds + r * pitch + k) = pack_8bit<X>(keep[j], rs.factor);
+            if (k == 0)
                 q_scale[r] = rs.scale;
         }
         __syncthreads();
     }
 
-    const int8_t *x[TILES];
+    v4i acc = v4i{};
+    auto products = [&](int s, const Group &f) {
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-        const int row = t * 16 + lane % 16 < g.rows ? t * 16 + lane % 16 : g.rows - 1;
-        x[t] = FUSED ? q_lds + row * pitch : g.x + (int64_t)row * g.x_stride;
-    }
-    v4i acc[TILES];
+        for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
-    for (int t = 0; t < TILES; ++t)
-        acc[t] = v4i{};
-    for (int s0 = wave; s0 < steps; s0 += 4 * AHEAD) {
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int step = s0 + 4 * i, k = step * 128 + k_lane;
-            if (step < steps) {
-#pragma unroll
-                for (int t = 0; t < TILES; ++t) {
-                    const v4i a = FUSED ? *(const v4i *)(x[t] + k) : piece(x[t], k);
-                    const v4i b = FUSED ? *(const v4i *)(x[t] + k + 16) : piece(x[t], k + 16);
-                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i][0], a, acc[t], 0, 0, 0);
-                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i][1], b, acc[t], 0, 0, 0);
-                }
-                fetch(step + 4 * AHEAD, wf[i]);
+            for (int h = 0; h < 2; ++h) {
+                const int k = (s + 4 * i) * 128 + lane / 16 * 16 + 64 * h;
+                v4i b = FUSED ? *(const v4i *)(x + (s + 4 * i < steps ? k : 0)) : f.x[i][h];
+                if (FUSED ? s + 4 * i >= steps : (s + 4 * i + 1) * 128 > g.k_end)
+                    b = k < g.k_end ? b : v4i{};
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i][h], b, acc, 0, 0, 0);
             }
+    };
+    for (int s = wave;; s += 8 * AHEAD) {
+        if (s + 4 * AHEAD >= steps) {
+            products(s, first);
+            break;
         }
+        fetch(s + 4 * AHEAD, second);
+        products(s, first);
+        if (s + 8 * AHEAD >= steps) {
+            products(s + 4 * AHEAD, second);
+            break;
+        }
+        fetch(s + 8 * AHEAD, first);
+        products(s + 4 * AHEAD, second);
     }
-    // a lane has outputs 4 (lane / 16) .. + 3 of token lane % 16
-#pragma unroll
-    for (int t = 0; t < TILES; ++t)
-        if (wave > 0)
-            *(v4i *)&sums[wave - 1][t][lane * 4] = acc[t];
-    __syncthreads();
+    // a lane has outputs 4 (lane / 16) to + 3 of row lane % 16
     if (wave > 0)
+        *(v4i *)&sums[wave - 1][lane * 4] = acc;
+    __syncthreads();
+    const int row = lane % 16, o = out0 + lane / 16 * 4;
+    if (wave > 0 || row >= g.rows)
         return;
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-        const int row = t * 16 + lane % 16, o = out0 + lane / 16 * 4;
-        v4i sum = acc[t];
+    for (int i = 0; i < 3; ++i)
+        acc += *(const v4i *)&sums[i][lane * 4];
+    const float xs = FUSED ? q_scale[row] : g.x_scale[row];
+    typename T::raw *y = (typename T::raw *)g.y + (int64_t)row * g.y_stride + o;
+    Pack<T, 4> out;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            sum += *(const v4i *)&sums[i][t][lane * 4];
-        if (row >= g.rows)
-            continue;
-        const float xs = FUSED ? q_scale[row] : g.x_scale[row];
-        typename T::raw *y = (typename T::raw *)g.y + (int64_t)row * g.y_stride + o;
-        Pack<T, 4> out;
+    for (int v = 0; v < 4; ++v) {
+        const int oo = o + v < g.outs ? o + v : g.outs - 1;
+        float f = (float)acc[v] * (xs * g.w_scale[oo]);
+        if (g.bias)
+            f += g.bias[oo];
+        out.v[v] = T::store(f);
+    }
+    if (o + 4 <= g.outs) {
+        store_pack<T, 4>(y, out);
+    } else {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int oo = o + v < g.outs ? o + v : g.outs - 1;
-            float f = (float)sum[v] * (xs * g.w_scale[oo]);
-            if (g.bias)
-                f += g.bias[oo];
-            out.v[v] = T::store(f);
-        }
-        if (o + 4 <= g.outs) {
-            store_pack<T, 4>(y, out);
-        } else {
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                if (o + v < g.outs)
-                    y[v] = out.v[v];
-        }
+        for (int v = 0; v < 4; ++v)
+            if (o + v < g.outs)
+                y[v] = out.v[v];
     }
 }
 
@@ -426,7 +449,7 @@ static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 static bool fused(const rnn_quant_desc &d)
 {
-    return d.x_dtype != RNN_DTYPE_I8 && d.rows <= 16 && d.rows * d.cols <= kFusedElements;
+    return d.x_dtype != RNN_DTYPE_I8 && d.cols > 0 && d.rows <= kFewRows && d.rows * pitch(d.cols) <= kFusedElements;
 }
 
 size_t project_workspace(const rnn_quant_desc &d)
@@ -452,24 +475,19 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
         const size_t lds = (size_t)g.rows * (pitch(cols) + 16) + g.rows * 4;
         switch (a.d.x_dtype) {
         case RNN_DTYPE_F32:
-            project_rows_kernel<T, F32, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            project_rows_kernel<T, F32><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
             break;
         case RNN_DTYPE_BF16:
-            project_rows_kernel<T, BF16, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            project_rows_kernel<T, BF16><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
             break;
         default:
-            project_rows_kernel<T, F16, 1><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
+            project_rows_kernel<T, F16><<<few, 256, lds, s>>>(g, a.x, a.d.x_stride, cols);
             break;
         }
         return (int)hipGetLastError();
     }
-    if (g.rows <= kFewRows) {
-        switch ((g.rows + 15) / 16) {
-        case 1: project_rows_kernel<T, NoSource, 1><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
-        case 2: project_rows_kernel<T, NoSource, 2><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
-        case 3: project_rows_kernel<T, NoSource, 3><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
-        default: project_rows_kernel<T, NoSource, 4><<<few, 256, 0, s>>>(g, nullptr, 0, cols); break;
-        }
+    if (g.rows <= kFewRows && cols > 0) {
+        project_rows_kernel<T, NoSource><<<few, 256, 0, s>>>(g, nullptr, 0, cols);
         return (int)hipGetLastError();
     }
     // The largest tiles that give most of the 256 compute units one.
