@@ -273,8 +273,7 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
 // ---------------------------------------------------------------------------
 // Few rows (up to 16, and at least a column).  A workgroup has 16 outputs; its four waves take steps
 // of 128 columns in turn and add their sums in LDS.  A load takes 64 bytes of
-// 16 weight rows, straight into the operands of 16x16x64 products; four steps
-// of both sides are in flight.  With FROM (the rows' type) x is rounded in the
+// 16 weight rows, straight into the operands of 16x16x64 products.  With FROM (the rows' type) x is rounded in the
 // call: each workgroup does it for itself, into LDS, while its first weights
 // are on their way; that is less than a launch for few elements.
 // ---------------------------------------------------------------------------
@@ -289,11 +288,11 @@ __global__ __launch_bounds__(256) void project_rows_kernel(ProjectGo g, const vo
                                                           int64_t source_stride, int32_t cols)
 {
     constexpr bool FUSED = !std::is_same<FROM, NoSource>::value;
-    constexpr int AHEAD = 4;                     // steps in flight
+    constexpr int AHEAD = 2;                     // steps of a group; two are in flight
     extern __shared__ __attribute__((aligned(16))) int8_t q_lds[];   // FUSED: rows of pitch, then scales
     __shared__ __attribute__((aligned(16))) int sums[3][256];
     __shared__ uint32_t row_max[16];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int out0 = blockIdx.x * 16;
     const int steps = (g.k_end + 127) / 128;
     const int pitch = steps * 128 + 16;
@@ -486,14 +485,18 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
         }
         return (int)hipGetLastError();
     }
-    if (g.rows <= kFewRows && cols > 0) {
+    auto tiles = [&](int64_t bm, int64_t bn) {
+        return (g.rows + bm - 1) / bm * ((g.outs + bn - 1) / bn);
+    };
+    // Each of its workgroups reads all of x: with 64 MiB of weights or more the
+    // tiles are faster (16 rows x 8192 columns x 16384 outputs: 22 us against
+    // 32; 8192 outputs of 2048 columns: 9.0 against 8.8 and no launch to round).
+    const bool heavy = (int64_t)g.outs * g.k_end >= (int64_t)64 << 20 && tiles(64, 64) >= 192;
+    if (g.rows <= kFewRows && cols > 0 && !heavy) {
         project_rows_kernel<T, NoSource><<<few, 256, 0, s>>>(g, nullptr, 0, cols);
         return (int)hipGetLastError();
     }
     // The largest tiles that give most of the 256 compute units one.
-    auto tiles = [&](int64_t bm, int64_t bn) {
-        return (g.rows + bm - 1) / bm * ((g.outs + bn - 1) / bn);
-    };
     if (tiles(64, 64) > 0x7fffffff)
         return (int)hipErrorInvalidConfiguration;
     if (tiles(256, 256) >= 192)

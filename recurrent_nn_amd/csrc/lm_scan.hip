@@ -112,55 +112,69 @@ template <int L> __device__ __forceinline__ float group_sum(float v)
 
 constexpr int64_t kFewSteps = 8;
 
-template <class T, int L> __global__ __launch_bounds__(256) void scan_steps_kernel(ScanArgs a,
-                                                                                 uint32_t row_blocks)
+// FOURS: the states divide by four, so that a lane's are one load.
+template <class T, int L, bool FOURS>
+__global__ __launch_bounds__(256) void scan_steps_kernel(ScanArgs a, uint32_t row_blocks,
+                                                        uint32_t per)
 {
     using raw = typename T::raw;
     const int64_t b = blockIdx.x / row_blocks;
-    const int64_t c = ((int64_t)(blockIdx.x % row_blocks) * 256 + threadIdx.x) / L;
+    const int64_t c = (blockIdx.x % row_blocks * 256ull + threadIdx.x) / L;
     const int n0 = threadIdx.x % L * 4;
     const int64_t steps = a.d.steps, len = row_length(a.lens, b, steps);
     const int N = (int)a.d.states;
+    // (with FOURS a lane has four states or none)
     if (c >= a.d.dim)
         return;
-    const bool whole = N % 4 == 0;
+    const bool mine = n0 < N;
+    auto real = [&](int i) { return FOURS ? mine : n0 + i < N; };
     const int64_t at = (b * a.d.dim + c) * N + n0;
-    const int64_t g = (uint32_t)c / (uint32_t)(a.d.dim / a.d.groups);
-    float h[4] = {}, A[4] = {};
-    if (whole && n0 < N) {
-        if (a.state_in)
-            __builtin_memcpy(h, __builtin_assume_aligned(a.state_in + at, 4), 16);
-        if (len > 0)
-            __builtin_memcpy(A, __builtin_assume_aligned(a.A + c * N + n0, 4), 16);
+    const uint32_t g = (uint32_t)c / per;       // per: channels of a group of B and C
+    // (no load depends on a condition: it would be waited for on the spot)
+    const int n_load = mine ? n0 : 0;
+    const float *A_at = a.A + c * N + n_load;
+    const float *h_at = a.state_in ? a.state_in + (b * a.d.dim + c) * N + n_load : A_at;
+    float h[4], A[4];
+    if (FOURS) {
+        __builtin_memcpy(h, __builtin_assume_aligned(h_at, 4), 16);
+        __builtin_memcpy(A, __builtin_assume_aligned(A_at, 4), 16);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n0 + i < N) {
-                h[i] = a.state_in ? a.state_in[at + i] : 0.0f;
-                A[i] = len > 0 ? a.A[c * N + n0 + i] : 0.0f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + i < N ? n0 + i - n_load : 0;
+            h[i] = h_at[n];
+            A[i] = A_at[n];
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        A[i] *= kLog2e;
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.0f;
     const float D = a.D ? a.D[c] : 0.0f;
     const raw *x = (const raw *)a.x + b * a.d.x_batch_stride + c;
     const raw *dt = (const raw *)a.dt + b * a.d.dt_batch_stride + c;
-    const raw *z = a.z ? (const raw *)a.z + b * a.d.z_batch_stride + c : nullptr;
-    const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + n0;
-    const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + n0;
+    // without a gate x is loaded in its place, and not used
+    const raw *z = a.z ? (const raw *)a.z + b * a.d.z_batch_stride + c : x;
+    const int64_t z_step = a.z ? a.d.z_step_stride : a.d.x_step_stride;
+    const raw *B = (const raw *)a.B + b * a.d.B_batch_stride + g * a.d.B_group_stride + n_load;
+    const raw *C = (const raw *)a.C + b * a.d.C_batch_stride + g * a.d.C_group_stride + n_load;
     raw *y = (raw *)a.y + b * a.d.y_batch_stride + c;
-    for (int64_t t = 0; t < len; ++t) {
-        float Bv[4] = {}, Cv[4] = {};
+    if (!a.state_in)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n0 + i < N) {
-                Bv[i] = T::load(B[t * a.d.B_step_stride + i]);
-                Cv[i] = T::load(C[t * a.d.C_step_stride + i]);
+            h[i] = 0.0f;
+    for (int64_t t = 0; t < len; ++t) {
+        Words4<T> Bw, Cw;
+        if (FOURS) {
+            Bw.load(B + t * a.d.B_step_stride);
+            Cw.load(C + t * a.d.C_step_stride);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = n0 + i < N ? n0 + i - n_load : 0;
+                Bw.set(i, B[t * a.d.B_step_stride + n]);
+                Cw.set(i, C[t * a.d.C_step_stride + n]);
             }
+        }
         const float xv = T::load(x[t * a.d.x_step_stride]);
-        const raw zv = z ? z[t * a.d.z_step_stride] : raw(0);
+        const raw zv = z[t * z_step];
         float s = T::load(dt[t * a.d.dt_step_stride]) + bias;
         if (a.d.dt_softplus)
             s = softplus(s);
@@ -168,14 +182,15 @@ template <class T, int L> __global__ __launch_bounds__(256) void scan_steps_kern
         float p = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (n0 + i < N) {
-                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * A[i]), h[i], sx * Bv[i]);
-                p = __builtin_fmaf(Cv[i], h[i], p);
+            if (real(i)) {
+                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * (A[i] * kLog2e)), h[i],
+                                      sx * Bw.get(i));
+                p = __builtin_fmaf(Cw.get(i), h[i], p);
             }
         p = group_sum<L>(p);
         if (a.D)
             p = __builtin_fmaf(D, xv, p);
-        if (z)
+        if (a.z)
             p *= silu(T::load(zv));
         if (n0 == 0)
             y[t * a.d.y_step_stride] = T::store(p);
@@ -185,14 +200,13 @@ template <class T, int L> __global__ __launch_bounds__(256) void scan_steps_kern
             y[t * a.d.y_step_stride] = T::store(0.0f);
     if (!a.state_out)
         return;
-    if (whole && n0 < N) {
+    if (FOURS && mine)
         __builtin_memcpy(__builtin_assume_aligned(a.state_out + at, 4), h, 16);
-    } else {
+    if (!FOURS)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (n0 + i < N)
                 a.state_out[at + i] = h[i];
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -592,13 +606,34 @@ template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp,
     return (int)hipGetLastError();
 }
 
+// No steps: the state is handed on.
+__global__ __launch_bounds__(256) void scan_no_steps_kernel(const float *in, float *out, int64_t n)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n)
+        out[i] = in ? in[i] : 0.0f;
+}
+
+static int no_steps_go(const ScanArgs &a, hipStream_t s)
+{
+    const int64_t n = a.d.batch * a.d.dim * a.d.states;
+    if ((n + 255) / 256 > 0x7fffffff)
+        return (int)hipErrorInvalidConfiguration;
+    scan_no_steps_kernel<<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a.state_in, a.state_out, n);
+    return (int)hipGetLastError();
+}
+
 template <class T, int L> static int steps_go(const ScanArgs &a, hipStream_t s)
 {
+    const uint32_t per = (uint32_t)(a.d.dim / a.d.groups);
     const int64_t row_blocks = (a.d.dim * L + 255) / 256;
     if (row_blocks * a.d.batch > 0x7fffffff)
         return (int)hipErrorInvalidConfiguration;
-    scan_steps_kernel<T, L><<<dim3((uint32_t)(row_blocks * a.d.batch)), dim3(256), 0, s>>>(
-        a, (uint32_t)row_blocks);
+    const dim3 grid((uint32_t)(row_blocks * a.d.batch)), block(256);
+    if (a.d.states % 4 == 0)
+        scan_steps_kernel<T, L, true><<<grid, block, 0, s>>>(a, (uint32_t)row_blocks, per);
+    else
+        scan_steps_kernel<T, L, false><<<grid, block, 0, s>>>(a, (uint32_t)row_blocks, per);
     return (int)hipGetLastError();
 }
 
@@ -629,6 +664,8 @@ template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
 
 int launch_scan(const ScanArgs &a, hipStream_t s)
 {
+    if (a.d.steps == 0)
+        return no_steps_go(a, s);
     switch (a.d.dtype) {
     case RNN_DTYPE_F32: return scan_type<F32>(a, s);
     case RNN_DTYPE_BF16: return scan_type<BF16>(a, s);
