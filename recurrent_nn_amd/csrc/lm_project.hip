@@ -25,8 +25,9 @@ struct ProjectGo {
 };
 
 // ---------------------------------------------------------------------------
-// Many rows.  A workgroup has BM tokens x BN outputs, WM x WN waves.  A step
-// is 64 columns: a tile row is 64 bytes of LDS, whose 16-byte pieces are
+// Many rows.  A workgroup has BM tokens x BN outputs, WM x WN waves, or WK of
+// them that take a part of the columns each.  A step is 64 columns (of each
+// part): a tile row is 64 bytes of LDS, whose 16-byte pieces are
 // permuted by the row (piece p of row r holds columns 16 (p xor r/4%4) on), so
 // that the sixteen rows that one pass of a 16-byte read takes (lanes 0-3, 12-15,
 // 20-23, 24-27, then the others) are in different banks.  The permutation is applied to the addresses that the direct loads
@@ -62,17 +63,21 @@ __device__ __forceinline__ void interleave(std::integer_sequence<int, I...>)
      ...);
 }
 
-template <class T, int BM, int BN, int WM, int WN, int BUFFERS>
-__global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g, uint32_t m_tiles,
+template <class T, int BM, int BN, int WM, int WN, int WK, int BUFFERS>
+__global__ __launch_bounds__(64 * WM * WN * WK) void project_tiles_kernel(ProjectGo g, uint32_t m_tiles,
                                                                     uint32_t n_tiles)
 {
     using raw = typename T::raw;
-    constexpr int THREADS = 64 * WM * WN, KB = 64;
+    constexpr int WAVES = WM * WN * WK, THREADS = 64 * WAVES, KB = 64;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;       // 32 x 32 tiles of a wave
-    constexpr int XP = BM * 4 / THREADS, WP = BN * 4 / THREADS;   // pieces a thread loads
-    constexpr int ON = TN * 32, OP = ON + 4;                  // epilogue: a row of a wave's outputs
-    static_assert(WM * WN * 32 * OP * 4 <= BUFFERS * (BM + BN) * KB, "epilogue fits the tiles' memory");
-    __shared__ __attribute__((aligned(128))) int8_t lds[BUFFERS * (BM + BN) * KB];
+    constexpr int XP = BM * 4 * WK / THREADS, WP = BN * 4 * WK / THREADS;   // pieces a thread loads
+    // Epilogue: rows of ON outputs, V of a thread (16 bytes), R rows a pass
+    constexpr int ON = TN * 32, OP = ON + 4, V = 16 / sizeof(raw), R = 64 / (ON / V);
+    constexpr int ROWS = WK == 1 ? TM * 32 : BM / WK, PASSES = ROWS / R;    // of a wave
+    constexpr int BUFFER = WK * (BM + BN) * KB;
+    constexpr int SUMS = (WK == 1 ? WAVES * 32 : WK * BM) * OP * 4;
+    static_assert(WK == 1 || (WM == 1 && WN == 1), "columns are divided among single waves");
+    __shared__ __attribute__((aligned(128))) int8_t lds[BUFFERS * BUFFER > SUMS ? BUFFERS * BUFFER : SUMS];
 
     // Tiles in bands of 8 tiles of tokens, each XCD (workgroups go to them in
     // turn) a run of adjacent ones: what runs at a time on an XCD shares rows of
@@ -84,53 +89,49 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
     const int row0 = (int)((band * 8 + in % high) * BM), out0 = (int)(in / high * BN);
 
     const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-    const int wm = wave / WN, wn = wave % WN;
+    const int wk = wave / (WM * WN), wm = wave / WN % WM, wn = wave % WN;
 
     // rows past the end repeat the last one; their outputs are not stored
     const int8_t *xp[XP], *wp[WP];
     int kx[XP], kw[WP];
 #pragma unroll
     for (int i = 0; i < XP; ++i) {
-        const int q = i * THREADS + tid, r = q / 4;
+        const int q = i * THREADS + tid, r = q / 4 % BM;
         const int row = row0 + r < g.rows ? row0 + r : g.rows - 1;
-        kx[i] = (q % 4 ^ (r / 4 & 3)) * 16;
+        kx[i] = q / (4 * BM) * KB + (q % 4 ^ (r / 4 & 3)) * 16;
         xp[i] = g.x + (int64_t)row * g.x_stride + kx[i];
     }
 #pragma unroll
     for (int i = 0; i < WP; ++i) {
-        const int q = i * THREADS + tid, r = q / 4;
+        const int q = i * THREADS + tid, r = q / 4 % BN;
         const int row = out0 + r < g.outs ? out0 + r : g.outs - 1;
-        kw[i] = (q % 4 ^ (r / 4 & 3)) * 16;
+        kw[i] = q / (4 * BN) * KB + (q % 4 ^ (r / 4 & 3)) * 16;
         wp[i] = g.w + (int64_t)row * g.w_stride + kw[i];
     }
     auto stage = [&](int k) {
-        int8_t *X = lds + k % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
+        int8_t *X = lds + k % BUFFERS * BUFFER, *W = X + WK * BM * KB;
 #pragma unroll
         for (int i = 0; i < XP; ++i)
-            load_to_lds(xp[i] + k * KB, X + (i * THREADS + wave * 64) * 16);
+            load_to_lds(xp[i] + k * (KB * WK), X + (i * THREADS + wave * 64) * 16);
 #pragma unroll
         for (int i = 0; i < WP; ++i)
-            load_to_lds(wp[i] + k * KB, W + (i * THREADS + wave * 64) * 16);
+            load_to_lds(wp[i] + k * (KB * WK), W + (i * THREADS + wave * 64) * 16);
     };
 
     // the scales of the epilogue's rows and columns, on their way from the start
-    constexpr int PASSES = 32 / (64 / (ON / 8));
-    const int o = out0 + wn * ON + lane % (ON / 8) * 8;
-    float ws[8], bs[8] = {}, xs[TM][PASSES];
+    const int o = out0 + wn * ON + lane % (ON / V) * V;
+    const int row_first = row0 + (WK == 1 ? wm * TM * 32 : wave * ROWS) + lane / (ON / V);
+    float ws[V], bs[V] = {}, xs[PASSES];
 #pragma unroll
-    for (int v = 0; v < 8; ++v) {
+    for (int v = 0; v < V; ++v) {
         const int col = o + v < g.outs ? o + v : g.outs - 1;
         ws[v] = g.w_scale[col];
         if (g.bias)
             bs[v] = g.bias[col];
     }
 #pragma unroll
-    for (int m = 0; m < TM; ++m)
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int row = row0 + (wm * TM + m) * 32 + lane / (ON / 8) + i * (64 / (ON / 8));
-            xs[m][i] = g.x_scale[row < g.rows ? row : g.rows - 1];
-        }
+    for (int i = 0; i < PASSES; ++i)
+        xs[i] = g.x_scale[row_first + i * R < g.rows ? row_first + i * R : g.rows - 1];
 
     v16i acc[TN][TM];
 #pragma unroll
@@ -143,7 +144,8 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
         v4i x[TM], w[TN];
     };
     auto fetch = [&](int k, int half, Half &f) {
-        const int8_t *X = lds + k % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
+        const int8_t *X = lds + k % BUFFERS * BUFFER + wk * BM * KB;
+        const int8_t *W = lds + k % BUFFERS * BUFFER + WK * BM * KB + wk * BN * KB;
         const int at = ((half * 2 + lane / 32) ^ (lane / 4 & 3)) * 16;
         X += (wm * TM * 32 + lane % 32) * KB + at;
         W += (wn * TN * 32 + lane % 32) * KB + at;
@@ -163,7 +165,7 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
     };
     using Products = std::make_integer_sequence<int, TM * TN>;
 
-    const int steps = g.k_end / KB;             // whole ones
+    const int steps = g.k_end / (KB * WK);      // whole ones
 #pragma unroll
     for (int k = 0; k < BUFFERS; ++k)
         if (k < steps)
@@ -204,9 +206,9 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
         products(even);
         products(odd);
     }
-    if (g.k_end % KB) {                         // the last columns, zeros behind them
-        const int k0 = steps * KB;
-        int8_t *X = lds + steps % BUFFERS * (BM + BN) * KB, *W = X + BM * KB;
+    if (g.k_end % (KB * WK)) {                  // the last columns, zeros behind them
+        const int k0 = steps * (KB * WK);
+        int8_t *X = lds + steps % BUFFERS * BUFFER, *W = X + WK * BM * KB;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < XP; ++i)
@@ -227,46 +229,67 @@ __global__ __launch_bounds__(64 * WM * WN) void project_tiles_kernel(ProjectGo g
     __syncthreads();
 
     // Epilogue.  A lane holds groups of four outputs of one token; through LDS
-    // (each wave its own part) it gets eight adjacent outputs of a token and
-    // stores them as one piece of a row.
-    int *tile = (int *)lds + wave * 32 * OP;
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {
+    // it gets V adjacent outputs of a token, and R rows go out as whole pieces.
+    // A wave uses a part of its own, 32 tokens at a time; waves with parts of the
+    // columns put down all their sums first, and each adds up some of the rows.
+    int *tile = (int *)lds + (WK == 1 ? wave * 32 : wk * BM) * OP;
+    auto put_down = [&](int m, int *to) {
 #pragma unroll
         for (int n = 0; n < TN; ++n)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                *(v4i *)(tile + lane % 32 * OP + n * 32 + 8 * v + 4 * (lane / 32)) =
+                *(v4i *)(to + lane % 32 * OP + n * 32 + 8 * v + 4 * (lane / 32)) =
                     v4i{acc[n][m][4 * v], acc[n][m][4 * v + 1], acc[n][m][4 * v + 2], acc[n][m][4 * v + 3]};
-        __builtin_amdgcn_wave_barrier();
-        const int t0 = row0 + (wm * TM + m) * 32;
+    };
+    auto pass = [&](int i, const int *from) {
+        v4i sum[V / 4];
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int r = lane / (ON / 8) + i * (64 / (ON / 8));
-            const v4i *from = (const v4i *)(tile + r * OP + lane % (ON / 8) * 8);
-            const v4i lo = from[0], hi = from[1];
-            const int row = t0 + r;
-            if (row >= g.rows)
-                continue;
-            Pack<T, 8> out;
+        for (int q = 0; q < V / 4; ++q) {
+            sum[q] = *(const v4i *)(from + 4 * q);
 #pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                float f = (float)(v < 4 ? lo[v % 4] : hi[v % 4]) * (xs[m][i] * ws[v]);
-                if (g.bias)
-                    f += bs[v];
-                out.v[v] = T::store(f);
-            }
-            raw *y = (raw *)g.y + (int64_t)row * g.y_stride + o;
-            if (o + 8 <= g.outs) {
-                store_pack<T, 8>(y, out);
-            } else {
-#pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    if (o + v < g.outs)
-                        y[v] = out.v[v];
-            }
+            for (int part = 1; part < WK; ++part)
+                sum[q] += *(const v4i *)(from + part * BM * OP + 4 * q);
         }
-        __builtin_amdgcn_wave_barrier();
+        const int row = row_first + i * R;
+        if (row >= g.rows)
+            return;
+        Pack<T, V> out;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f = (float)sum[v / 4][v % 4] * (xs[i] * ws[v]);
+            if (g.bias)
+                f += bs[v];
+            out.v[v] = T::store(f);
+        }
+        raw *y = (raw *)g.y + (int64_t)row * g.y_stride + o;
+        if (o + V <= g.outs) {
+            store_pack<T, V>(y, out);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (o + v < g.outs)
+                    y[v] = out.v[v];
+        }
+    };
+    const int at = lane / (ON / V) * OP + lane % (ON / V) * V;
+    if constexpr (WK == 1) {
+#pragma unroll
+        for (int m = 0; m < TM; ++m) {
+            put_down(m, tile);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < 32 / R; ++i)
+                pass(m * (32 / R) + i, tile + i * R * OP + at);
+            __builtin_amdgcn_wave_barrier();
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+            put_down(m, tile + m * 32 * OP);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i)
+            pass(i, (const int *)lds + (wave * ROWS + i * R) * OP + at);
     }
 }
 
@@ -458,12 +481,13 @@ size_t project_workspace(const rnn_quant_desc &d)
     return up256((size_t)d.rows * pitch(d.cols)) + up256((size_t)d.rows * 4);
 }
 
-template <class T, int BM, int BN, int WM, int WN, int BUFFERS>
+template <class T, int BM, int BN, int WM, int WN, int WK, int BUFFERS>
 static void tiles_go(const ProjectGo &g, hipStream_t s)
 {
     const uint32_t m = (uint32_t)((g.rows + (int64_t)BM - 1) / BM);
     const uint32_t n = (uint32_t)((g.outs + (int64_t)BN - 1) / BN);
-    project_tiles_kernel<T, BM, BN, WM, WN, BUFFERS><<<dim3(m * n), dim3(64 * WM * WN), 0, s>>>(g, m, n);
+    project_tiles_kernel<T, BM, BN, WM, WN, WK, BUFFERS>
+        <<<dim3(m * n), dim3(64 * WM * WN * WK), 0, s>>>(g, m, n);
 }
 
 template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &a, hipStream_t s)
@@ -496,15 +520,21 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
         project_rows_kernel<T, NoSource><<<few, 256, 0, s>>>(g, nullptr, 0, cols);
         return (int)hipGetLastError();
     }
-    // The largest tiles that give most of the 256 compute units one.
+    // The largest tiles that give most of the 256 compute units one.  The smallest
+    // ones, if they are all there at once, with the columns divided among the
+    // waves, a quarter of the steps (2238 rows x 6607 columns x 68 outputs: 14.7
+    // us against 17.5; with more tiles than that its memory of LDS, one workgroup
+    // a unit, costs more: 777 x 1500 x 2101 13.2 against 10.6).
     if (tiles(64, 64) > 0x7fffffff)
         return (int)hipErrorInvalidConfiguration;
     if (tiles(256, 256) >= 192)
-        tiles_go<T, 256, 256, 2, 4, 4>(g, s);
+        tiles_go<T, 256, 256, 2, 4, 1, 4>(g, s);
     else if (tiles(128, 128) >= 192)
-        tiles_go<T, 128, 128, 2, 2, 4>(g, s);
+        tiles_go<T, 128, 128, 2, 2, 1, 4>(g, s);
+    else if (tiles(64, 64) > 256)
+        tiles_go<T, 64, 64, 2, 2, 1, 4>(g, s);
     else
-        tiles_go<T, 64, 64, 2, 2, 4>(g, s);
+        tiles_go<T, 64, 64, 1, 1, 4, 3>(g, s);
     return (int)hipGetLastError();
 }
 
