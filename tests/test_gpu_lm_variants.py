@@ -1,0 +1,163 @@
+"""The language-model operators where their kernels change form: every tile of
+the projection with columns and rows that end inside it, few rows beside many
+weights, spans of the scan, channel groups that fill no workgroup, states in
+place; against the plain 64-bit definitions (tests/lm_ref.py), or, where those
+would take long, against exact integer arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import recurrent_nn_amd as ra
+from tests import lm_ref
+from tests.lm_ref import assert_close
+from tests.test_gpu_lm import (BF16, F16, F32, INF, NAN, Draw, _gpu, check_scores, cuda,  # noqa: F401
+                               inside, scan_call, scan_inputs, weights)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows,cols,outs,dtype", [
+    (2048, 96, 6144 + 7, F32),         # 256 x 256 tiles, a step and a half of columns
+    (3500, 335, 3600, BF16),
+    (4096, 64, 4096, F16), (1700, 272, 1500, F32),      # 128 x 128
+    (900, 500, 1500, BF16),            # 64 x 64, more than 256
+    (70, 255, 70, F32), (70, 256, 70, F16), (70, 257, 70, BF16), (90, 1040, 33, F32),
+    (17, 3000, 129, F32), (500, 16, 200, BF16)])         # columns among the waves
+def test_projection_tiles(rows, cols, outs, dtype):
+    r = Draw(rows + 3 * cols + 7 * outs)
+    q = torch.randint(-127, 128, (rows, cols), generator=r.g, dtype=torch.int8)
+    x = torch.zeros(rows, (cols + 15) // 16 * 16, dtype=torch.int8)
+    x[:, :cols] = q
+    w, wd, ws = weights(r, outs, cols)
+    xs, bias = r.uniform(rows, lo=0.5, hi=1.5), r.normal(outs)
+    got = ra.quant_project(x.cuda()[:, :cols], wd, ws.cuda(), bias=bias.cuda(), x_scale=xs.cuda(),
+                           out_dtype=dtype)
+    # in 64 bits: the sums pass 2^24
+    total = (q.cuda().double() @ w.cuda().double().t()).cpu().numpy()
+    y = total * xs.double().numpy()[:, None] * ws.double().numpy()
+    err = 4 * lm_ref.U * np.abs(y)
+    y = y + bias.double().numpy()
+    assert_close(got, y, lm_ref.stored(y, 2 * (err + 2 * lm_ref.U * np.abs(y)), dtype), "y")
+
+
+@pytest.mark.parametrize("rows", [1, 3, 16])
+def test_projection_of_few_rows_and_many_weights(rows):
+    r = Draw(rows)
+    cols, outs = 4100, 16400                   # more than 64 MiB of them
+    q = torch.randint(-127, 128, (rows, cols), generator=r.g, dtype=torch.int8)
+    x = torch.zeros(rows, 4112, dtype=torch.int8)
+    x[:, :cols] = q
+    w, wd, ws = weights(r, outs, cols)
+    got = ra.quant_project(x.cuda()[:, :cols], wd, ws.cuda(), x_scale=torch.ones(rows).cuda())
+    total = (q.double() @ w.double().t()).numpy()
+    y = total * ws.double().numpy()
+    assert_close(got, y, lm_ref.stored(y, 8 * lm_ref.U * np.abs(y), F32), "y")
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 8), (1, 16384), (2, 8192), (16, 1024), (16, 1000), (5, 3),
+                                       (16, 1025), (3, 5462)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_rounded_inside_are_the_rounded_rows(rows, cols, dtype):
+    r = Draw(rows * cols)
+    x = r.normal(rows, cols, dtype=dtype)
+    if rows > 2:
+        x[1] = 0
+        x[2, cols - 1] = INF
+    _, wd, ws = weights(r, 40, cols)
+    q = ra.quantize_rows(x.cuda())
+    want = ra.quant_project(q.q, wd, ws.cuda(), x_scale=q.scale, out_dtype=dtype)
+    got = ra.quant_project(inside(x, 3), wd, ws.cuda())
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(got[keep], want[keep])
+    assert rows <= 2 or torch.isnan(got[2]).all()
+
+
+SPANS = [  # batch, steps, dim, states, groups, dtype, softplus, bias, skip, gate, state, lens
+    (1, 900, 16, 16, 1, F32, True, True, True, True, True, False),
+    (3, 700, 20, 16, 1, F32, True, True, True, True, True, True),
+    (2, 1000, 30, 7, 2, F32, True, True, False, False, True, True),
+    (1, 1200, 24, 40, 3, F32, True, True, True, True, False, False),
+    (2, 800, 16, 64, 1, BF16, True, True, True, True, True, True),
+    (2, 640, 33, 48, 11, F32, False, False, True, False, True, True),
+]
+
+
+@pytest.mark.parametrize("k", range(len(SPANS)))
+def test_scan_in_spans(k):
+    spec = SPANS[k]
+    v = scan_inputs(Draw(900 + k), *spec)
+    if v["lens"] is not None:              # one that ends at a span's border, one within the first
+        v["lens"][1:] = torch.tensor([128, 5][:len(v["lens"]) - 1])
+    y, err, h, herr = lm_ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["z"],
+                                  v["dt_bias"], spec[6], v["state"], v["lens"])
+    got, gh = scan_call(v, spec[6])
+    assert_close(got, y, err, "y")
+    assert_close(gh, h, herr, "state")
+    if v["state"] is not None:             # the state in place, while spans read it
+        hold = cuda(v["state"]).clone()
+        again, _ = scan_call(v, spec[6], state=hold, state_out=hold)
+        assert torch.equal(again, got) and torch.equal(hold, gh)
+
+
+@pytest.mark.parametrize("steps", [1, 8, 9, 15, 16, 63, 64, 65, 127])
+@pytest.mark.parametrize("states", [16, 5])
+def test_scan_lengths_around_its_tiles(steps, states):
+    spec = (2, steps, 19, states, 1, F32, True, True, True, True, True, True)
+    v = scan_inputs(Draw(steps), *spec)
+    v["lens"][1] = steps // 2
+    y, err, h, herr = lm_ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["z"],
+                                  v["dt_bias"], True, v["state"], v["lens"])
+    got, gh = scan_call(v, True)
+    assert_close(got, y, err, "y")
+    assert_close(gh, h, herr, "state")
+
+
+@pytest.mark.parametrize("states", [16, 13, 40])
+def test_scan_infinities_keep_to_their_channel_and_time(states):
+    spec = (1, 200, 48, states, 1, F32, True, True, True, True, True, False)
+    v = scan_inputs(Draw(77), *spec)
+    clean, _ = scan_call(v, True)
+    v["x"][0, 70, 20] = -INF
+    got, state = scan_call(v, True)
+    bad = torch.zeros(1, 200, 48, dtype=torch.bool)
+    bad[0, 70:, 20] = True
+    assert torch.equal(got.cpu()[~bad], clean.cpu()[~bad])
+    assert not torch.isfinite(got[0, 70, 20]) and torch.isfinite(state[0, :20]).all()
+
+
+def test_convolution_of_odd_channels_with_its_window_in_place():
+    r = Draw(5)
+    for dim in (1, 2, 3, 5, 7, 33):
+        for dtype in (F32, BF16):
+            x, w = r.normal(3, 40, dim, dtype=dtype), r.normal(dim, 4)
+            state = r.normal(3, 3, dim, dtype=dtype)
+            y, err, win = lm_ref.conv(x, w, None, True, state, None)
+            hold = state.cuda()
+            got, _ = ra.causal_conv(inside(x, 1), w.cuda(), silu=True, state=hold, state_out=hold)
+            assert_close(got, y, err, "y")
+            assert_close(hold, win, 0, "window")
+
+
+@pytest.mark.parametrize("rows,vocab,top,dtype", [
+    (1, 262144, 64, F32), (1, 8193, 3, BF16), (2, 16391, 64, F16), (7, 65539, 1, BF16),
+    (520, 9001, 20, F32), (3, 8, 8, F32), (3, 7, 2, BF16), (2, 2049, 64, F32)])
+def test_scores_in_segments_and_odd_ends(rows, vocab, top, dtype):
+    r = Draw(vocab + top)
+    x = r.normal(rows, vocab, scale=3.0, dtype=dtype)
+    x[0, -1] = 20.0                         # the best entry is the last one
+    tokens = torch.randint(0, vocab, (rows,), generator=r.g)
+    tokens[0] = vocab - 1
+    check_scores(x, tokens, top, pad=1)
+
+
+def test_scores_of_equal_entries_over_segments():
+    x = torch.zeros(2, 70001)
+    x[1, 40000:] = 1.0
+    x[1, 69990] = NAN
+    check_scores(x, torch.tensor([70000, 69990]), 64)
+    y = torch.full((3, 70001), -INF)        # a mask that leaves one, two, no entries
+    y[0, 69999] = -3.0
+    y[1, 5] = y[1, 60000] = 2.0
+    check_scores(y, torch.tensor([69999, 60000, 4]), 20)
+    check_scores(y.to(BF16), torch.tensor([5, 5, 70000]), 5)
