@@ -4,12 +4,16 @@ Every HIP source is compiled by hipcc for --offload-arch=gfx950 with
 -ffp-contract=off (the gate arithmetic must not fuse multiplies into adds)
 and with the packed-fp32 instructions disabled; the host-only plan code is
 plain C++17.  Objects go to _build/ (not versioned), the library next to this
-file, where the Python binding loads it.
+file, where the Python binding loads it.  The compiled part of the torch
+binding (csrc/binding.cpp: host code, on torch's own headers) is an extension
+module beside it.
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -51,6 +55,7 @@ HIP_UNITS = ([(f, [], f + ".o") for f in sorted(os.listdir(CSRC))
                f"recurrence_inst_f{fam}_a{act}.o") for fam, act in INST_UNITS] +
              [("run.cpp", [], "run.cpp.o"), ("lm_run.cpp", [], "lm_run.cpp.o")])
 CXX_UNITS = [("plan.cpp", [], "plan.cpp.o")]
+BINDING = os.path.join(HERE, "_binding.so")
 
 
 def _compile(unit, verbose, build_dir=BUILD, defs=()):
@@ -76,11 +81,32 @@ STAMPS_BUILD = os.path.join(ROOT, "_build", "recurrent_nn_amd_stamps")
 STAMPS_LIB = os.path.join(HERE, "librecurrent_nn_amd_stamps.so")
 
 
+def build_binding(verbose: bool = False) -> str:
+    """The extension module recurrent_nn_amd._binding."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared",
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, jobs: int = 8, stamps: bool = False) -> str:
     build_dir, lib, defs = (STAMPS_BUILD, STAMPS_LIB, ["-DRNN_STAMPS"]) if stamps else (BUILD, LIB, [])
     os.makedirs(build_dir, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = None if stamps else ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda u: _compile(u, verbose, build_dir, defs), HIP_UNITS + CXX_UNITS))
+    if binding:
+        binding.result()
     tmp = lib + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

@@ -6,6 +6,11 @@ Tensors live on one HIP device; the work goes to ``stream`` (default: torch's
 current stream of that device) and nothing waits for it.  What a call returns
 is new unless ``out`` / ``state_out`` supply it.  ValueError for tensors of
 the wrong kind, RNNError for what the library refuses.
+
+A call on the current device's current stream, with every tensor as it should
+be, is checked and made by the compiled module _binding (csrc/binding.cpp) in
+one step.  What it does not take (it returns None and has done nothing) goes
+the way below, with the same steps.
 """
 from __future__ import annotations
 
@@ -43,6 +48,34 @@ def _ptr(t) -> int:
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_ENTRIES = ("rnn_conv_run", "rnn_scan_workspace_size", "rnn_scan_run", "rnn_quantize_rows",
+            "rnn_quant_workspace_size", "rnn_quant_project", "rnn_scores_workspace_size",
+            "rnn_token_scores")
+_bound = None
+
+
+def _bind():
+    """The compiled module, with the entry points of the loaded library."""
+    global _bound
+    lib = _lib.load()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("recurrent_nn_amd/_binding.so is missing: build it with "
+                           "`python recurrent_nn_amd/build.py` (or __graft_entry__.build())") from e
+    _binding.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES])
+    _bound = _binding
+    return _bound
+
+
+def _done(r, where):
+    """The outputs of a compiled call; RNNError for a status."""
+    if type(r) is int:
+        _check(r, where)
+    return r
 
 
 def _on(tensors, stream, call):
@@ -116,6 +149,12 @@ def causal_conv(x, weight, bias=None, silu: bool = False, state=None, sequence_l
     type, the inputs before each row's length.  One new token: steps = 1.
     ``state_out`` may be ``state``.
     """
+    if stream is None and getattr(x, "is_cuda", False):
+        device = _device()
+        r = (_bound or _bind()).conv(x, weight, bias, silu, state, sequence_lens, out, state_out,
+                                     device, _raw_stream(device))
+        if r is not None:
+            return _done(r, "rnn_conv_run")
     lib = _lib.load()
     key = ("conv", _sig(x), _sig(weight), _sig(bias), _sig(state), _sig(out), _sig(state_out), silu)
     known = _known.get(key)
@@ -162,6 +201,12 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     states] float32; sequence_lens as in :func:`causal_conv`.  Returns (y,
     state_out).  One new token: steps = 1.  ``state_out`` may be ``state``.
     """
+    if stream is None and getattr(x, "is_cuda", False):
+        device = _device()
+        r = (_bound or _bind()).scan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, state, sequence_lens,
+                                     out, state_out, device, _raw_stream(device))
+        if r is not None:
+            return _done(r, "rnn_scan_run")
     lib = _lib.load()
     key = ("scan", _sig(x), _sig(dt), _sig(A), _sig(B), _sig(C), _sig(D), _sig(z), _sig(dt_bias),
            _sig(state), _sig(out), _sig(state_out), dt_softplus)
@@ -217,6 +262,11 @@ class QuantRows(NamedTuple):
 def quantize_rows(x, stream=None) -> QuantRows:
     """The rows of x [rows, cols] in 8 bits with one scale each (weights: a row
     is an output channel; activations: a row is a token)."""
+    if stream is None and getattr(x, "is_cuda", False):
+        device = _device()
+        r = (_bound or _bind()).quantize(x, device, _raw_stream(device))
+        if r is not None:
+            return QuantRows._make(_done(r, "rnn_quantize_rows"))
     lib = _lib.load()
     _data("x", x, 2)
     rows, cols = x.shape
@@ -257,6 +307,12 @@ def quant_project(x, w, w_scale, bias=None, x_scale=None, out_dtype: Optional[to
     bias [outs] float32.  y is in ``out_dtype`` (default: x's type, float32
     for int8 rows).
     """
+    if stream is None and getattr(x, "is_cuda", False):
+        device = _device()
+        r = (_bound or _bind()).project(x, w, w_scale, bias, x_scale, out_dtype, out, device,
+                                        _raw_stream(device))
+        if r is not None:
+            return _done(r, "rnn_quant_project")[0]
     lib = _lib.load()
     key = ("project", _sig(x), _sig(w), _sig(w_scale), _sig(bias), _sig(x_scale), out_dtype, _sig(out))
     known = _known.get(key)
@@ -318,6 +374,11 @@ def token_scores(logits, tokens=None, top: int = 0, stream=None) -> TokenScores:
     """Log probability and rank of given tokens, entropy, and the ``top`` most
     likely entries (equal ones in the order of their index) of each row of
     logits [rows, vocab]; tokens [rows] int32 or int64, or None."""
+    if stream is None and getattr(logits, "is_cuda", False):
+        device = _device()
+        r = (_bound or _bind()).scores(logits, tokens, top, device, _raw_stream(device))
+        if r is not None:
+            return TokenScores._make(_done(r, "rnn_token_scores"))
     lib = _lib.load()
     key = ("scores", _sig(logits), _sig(tokens), top)
     known = _known.get(key)
