@@ -110,14 +110,13 @@ __device__ __forceinline__ RowScale row_scale(float most, bool finite)
     return {127.0f / most, most / 127.0f};
 }
 
-// The largest of a wave's values, in all lanes.  (Magnitudes order as their bits
-// do, infinities and NaN above all finite ones.)
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+// A value of the wave's 64 lanes together, in all of them: op(own, other) with
+// other = `none` (which changes nothing) where a lane has no partner.
+template <class F> __device__ __forceinline__ uint32_t over_wave(uint32_t v, uint32_t none, F op)
 {
-    auto with = [&](auto ctrl, auto rows) {     // what has no lane to come from is 0
-        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(
-            0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-        v = o > v ? o : v;
+    auto with = [&](auto ctrl, auto rows) {
+        v = op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, decltype(ctrl)::value,
+                                                        decltype(rows)::value, 0xF, false));
     };
     with(std::integral_constant<int, 0xB1>{}, std::integral_constant<int, 0xF>{});    // lane xor 1
     with(std::integral_constant<int, 0x4E>{}, std::integral_constant<int, 0xF>{});    // lane xor 2
@@ -126,6 +125,21 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     with(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row 0 to 1, 2 to 3
     with(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // rows 0, 1 to 2, 3
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// (Magnitudes order as their bits do, infinities and NaN above all finite ones.)
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    return over_wave(v, 0u, [](uint32_t a, uint32_t b) { return b > a ? b : a; });
+}
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v)
+{
+    return over_wave(v, 0u, [](uint32_t a, uint32_t b) { return a + b; });
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+    return __uint_as_float(over_wave(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 constexpr uint32_t kInfBits = 0x7F800000u;
 

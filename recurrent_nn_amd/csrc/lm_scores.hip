@@ -65,23 +65,28 @@ struct Part {               // of a segment of a row
 // The parts of a workgroup's 256 threads together, in every thread.
 __device__ __forceinline__ Part over_workgroup(Part p, Part (&parts)[4])
 {
-#pragma unroll
-    for (int m = 32; m > 0; m /= 2) {
-        const Sums o{__shfl_xor(p.s.m, m, 64), __shfl_xor(p.s.sum, m, 64),
-                     __shfl_xor(p.s.cross, m, 64)};
-        p.s.join(o);
-        p.before += __shfl_xor(p.before, m, 64);
-    }
+    p.s.rebase(value_of(wave_max(value_key(p.s.m))));
+    p.s.sum = wave_sum(p.s.sum);
+    p.s.cross = wave_sum(p.s.cross);
+    p.before = wave_sum(p.before);
     if (threadIdx.x % 64 == 0)
         parts[threadIdx.x / 64] = p;
     __syncthreads();
-    p = parts[0];
+    Part all = parts[0];
 #pragma unroll
-    for (int i = 1; i < 4; ++i) {
-        p.s.join(parts[i].s);
-        p.before += parts[i].before;
+    for (int i = 1; i < 4; ++i)
+        all.s.m = __builtin_fmaxf(all.s.m, parts[i].s.m);
+    all.s.sum = all.s.cross = 0.0f;
+    all.before = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        Part o = parts[i];
+        o.s.rebase(all.s.m);
+        all.s.sum += o.s.sum;
+        all.s.cross += o.s.cross;
+        all.before += o.before;
     }
-    return p;
+    return all;
 }
 
 // The best `top` of the keys given to it, in order.  All threads of a
@@ -109,6 +114,23 @@ struct Best {
             if (at < kList)
                 list[at] = key;
         }
+    }
+    // N keys at once, those of `wanted` (a bit each): one addition to the count.
+    template <int N> __device__ __forceinline__ void offer(const uint64_t (&key)[N], uint32_t wanted)
+    {
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+            wanted &= ~((uint32_t)!(key[v] > bound) << v);
+        if (wanted == 0)
+            return;
+        uint32_t at = atomicAdd(count, (uint32_t)__popc(wanted));
+#pragma unroll
+        for (int v = 0; v < N; ++v)
+            if (wanted >> v & 1) {
+                if (at < kList)
+                    list[at] = key[v];
+                ++at;
+            }
     }
     // How many have been offered in all since the last order(); the caller
     // gives up on what did not fit with forget().
@@ -353,10 +375,10 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
     Best best;
     best.begin(list, sorted, &count, top);
     if (top > 0) {
-        // The bound, to 24 bits: the largest t that enough lanes reach.
+        // The bound, to 16 bits: the largest t that enough lanes reach.
         const uint32_t key = value_key(top_of_all), enough = (top + 3) / 4;
         uint32_t t = 0;
-        for (uint32_t bit = 1u << 31; bit >= 1u << 8; bit /= 2)
+        for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit /= 2)
             if (__popcll(__ballot(key >= (t | bit))) >= (int)enough)
                 t |= bit;
         if (lane == 0)
@@ -365,7 +387,7 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             t = bounds[i] < t ? bounds[i] : t;
-        // (cut to 24 bits, -inf lies below every number's key)
+        // (cut to 16 bits, -inf lies below every number's key)
         const float edge = t < value_key(kLowest) ? -__builtin_inff() : value_of(t);
         if (!odd && batches > 0)
             for (uint32_t s = 0; s < PARTS; ++s)
@@ -394,11 +416,15 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
             Pack<T, 8> pk{};
             if (on)
                 pk = logits_pack<T>(x, i, V);
+            uint64_t keys[8];
+            uint32_t want = 0;
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
                 const float f = T::load(pk.v[v]);
-                best.offer(order_key(f, 8 * i + v), on && 8 * i + v < V && wanted(f));
+                keys[v] = order_key(f, 8 * i + v);
+                want |= (uint32_t)(on && 8 * i + v < V && wanted(f)) << v;
             }
+            best.offer(keys, want);
             n = best.offered();
             if (n > kList) {            // too many at once: an eighth of them at a time
                 best.forget();
