@@ -256,14 +256,20 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
     __shared__ __attribute__((aligned(16))) float sh_B[2][16 * S * BP],
         sh_C[OUT ? 2 : 1][OUT ? 16 * S * BP : 1];
 
-    // Workgroups go to the 8 XCDs in turn: give each XCD adjacent channels, whose
-    // 32-byte pieces of a row share cache lines.
+    // Workgroups go to the 8 XCDs in turn: each XCD gets a run of this order, in
+    // which four workgroups of adjacent channels (their pieces of a row share
+    // cache lines) follow each other, then the spans, then the batch rows, and
+    // the rows of the next four channel groups from another row on: the long
+    // rows of a ragged batch are then spread over XCDs and compute units.
     const uint32_t total = gridDim.x, xcd = blockIdx.x % 8, q8 = total / 8, r8 = total % 8;
     const uint32_t id = xcd * q8 + (xcd < r8 ? xcd : r8) + blockIdx.x / 8;
-    const uint32_t g = id % sp.groups16 / sp.per16, part = id % sp.groups16 % sp.per16;
+    const uint32_t batch = (uint32_t)a.d.batch, each4 = 4 * sp.count * batch;
+    const uint32_t four = id / each4, left = sp.groups16 - 4 * four, wide = left < 4 ? left : 4;
+    const uint32_t in = id % each4, row = in / wide / sp.count;
+    const uint32_t channels = 4 * four + in % wide, span = in / wide % sp.count;
+    const int64_t b = (row + (uint64_t)four * (batch / 2 + 1)) % batch;
+    const uint32_t g = channels / sp.per16, part = channels % sp.per16;
     const int64_t c0 = (int64_t)g * sp.per + part * 16, c_end = (int64_t)(g + 1) * sp.per;
-    const uint32_t span = id / sp.groups16 % sp.count;
-    const int64_t b = id / sp.groups16 / sp.count;
     const int64_t steps = a.d.steps, dim = a.d.dim;
     const int N = (int)a.d.states;
     const int64_t len = row_length(a.lens, b, steps);
@@ -650,7 +656,7 @@ template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
     }
     Spans sp{};
     spans_of(a.d, sp);
-    if ((__int128)sp.groups16 * sp.count * a.d.batch > 0x7fffffff)
+    if ((__int128)sp.groups16 * sp.count * a.d.batch > 0x1fffffff)       // (four times it in 32 bits)
         return (int)hipErrorInvalidConfiguration;
     sp.state = (float *)a.workspace;
     sp.sum = sp.state + (size_t)a.d.batch * (sp.count + 1) * a.d.dim * a.d.states;
