@@ -403,7 +403,7 @@ rnn_status rnn_scan_run(const rnn_scan_desc *desc, void *hip_stream, void *works
  *   channel), activations that several projections share once for each token.
  *   Errors: RNN_ERR_INVALID_INPUT for sizes below 0, strides or dtype outside
  *   their ranges, a missing or misaligned tensor; RNN_ERR_UNSUPPORTED for
- *   2^31 rows or more.
+ *   2^31 rows or more, or a q_stride above 2^30.
  */
 rnn_status rnn_quantize_rows(void *hip_stream, int64_t rows, int64_t cols, int32_t dtype,
                              const void *x, int64_t x_stride, int8_t *q, int64_t q_stride,

@@ -283,6 +283,8 @@ extern "C" rnn_status rnn_quantize_rows(void *hip_stream, int64_t rows, int64_t 
         strides("q", rows, q_stride, 1, 0, q_stride, true);
         if (rows > 0x7fffffff)
             unsupported("2^31 rows or more");
+        if (q_stride > (int64_t)1 << 30)
+            unsupported("rows of more than 2^30 columns");
         if (rows == 0)
             return;
         pointer("x", x, elem_size(dtype), cols > 0);

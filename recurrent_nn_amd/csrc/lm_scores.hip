@@ -11,6 +11,7 @@
 // `top` elements reach, so that only the parts that reach it are read again
 // (a few more than `top`, from the caches), and what they hold above it is
 // ordered.  Few rows are cut into segments, which a second launch joins.
+// 1024 x 131072 in bf16: 58 us with 20 alternatives (4.6 TB/s), 53 with none.
 #include "lm_common.h"
 
 namespace rnnamd {

@@ -2,7 +2,7 @@
 binding of rnn_conv_run, rnn_scan_run, rnn_quantize_rows, rnn_quant_project
 and rnn_token_scores (include/recurrent_nn_amd.h has their definitions).
 
-Tensors live on one HIP device; the work goes to ``stream`` (default: torch's
+Forward only: nothing is recorded for gradients.  Tensors live on one HIP device; the work goes to ``stream`` (default: torch's
 current stream of that device) and nothing waits for it.  What a call returns
 is new unless ``out`` / ``state_out`` supply it.  ValueError for tensors of
 the wrong kind, RNNError for what the library refuses.
@@ -164,6 +164,8 @@ def causal_conv(x, weight, bias=None, silu: bool = False, state=None, sequence_l
         if weight.dim() != 2:
             raise ValueError("weight must be [dim, taps]")
         k = weight.shape[1]
+        if k < 1:
+            raise ValueError("weight must have a tap at least")
         _expect("weight", weight, (d, k), torch.float32, x.device)
         if bias is not None:
             _expect("bias", bias, (d,), torch.float32, x.device)

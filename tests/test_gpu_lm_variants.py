@@ -161,3 +161,38 @@ def test_scores_of_equal_entries_over_segments():
     y[1, 5] = y[1, 60000] = 2.0
     check_scores(y, torch.tensor([69999, 60000, 4]), 20)
     check_scores(y.to(BF16), torch.tensor([5, 5, 70000]), 5)
+
+
+def test_the_plain_call_and_the_other_way_are_the_same():
+    # a stream of the caller's goes through Python, no stream through the compiled binding
+    r = Draw(31)
+    here = torch.cuda.current_stream()
+    x, w = r.normal(2, 70, 48, dtype=BF16).cuda(), r.normal(48, 4).cuda()
+    v = scan_inputs(r, 2, 70, 48, 16, 1, BF16, True, True, True, True, True, True)
+    v = {k: cuda(t) for k, t in v.items()}
+    _, wd, ws = weights(r, 33, 48)
+    ws = ws.cuda()
+    logits = r.normal(5, 3000).cuda()
+    calls = [
+        lambda s: ra.causal_conv(x, w, silu=True, stream=s),
+        lambda s: ra.selective_scan(v["x"], v["dt"], v["A"], v["B"], v["C"], D=v["D"], z=v["z"],
+                                    dt_bias=v["dt_bias"], dt_softplus=True, state=v["state"],
+                                    sequence_lens=v["lens"], stream=s),
+        lambda s: ra.quantize_rows(x[0, :, :41], stream=s),
+        lambda s: [ra.quant_project(x[0], wd, ws, out_dtype=F16, stream=s)],
+        lambda s: [ra.quant_project(x.flatten(0, 1), wd, ws, stream=s)],
+        lambda s: ra.token_scores(logits, torch.arange(5).cuda(), top=4, stream=s),
+        lambda s: ra.token_scores(logits, torch.arange(5, dtype=torch.int32).cuda(), stream=s),
+    ]
+    for call in calls:
+        got, want = call(None), call(here)
+        assert type(got) is type(want) and len(got) == len(want)
+        for a, b in zip(got, want):
+            assert a.dtype == b.dtype and a.shape == b.shape and a.stride() == b.stride()
+            assert torch.equal(a, b)
+    assert ra.token_scores(logits, top=2).logprob is None
+    with pytest.raises(ValueError, match="tap"):
+        ra.causal_conv(x, w[:, :0])
+    with pytest.raises(ra.RNNError) as e:                # refused by the library in a compiled call
+        ra.causal_conv(x, torch.zeros(48, 9).cuda())
+    assert e.value.status == ra.RNN_ERR_INVALID_INPUT
