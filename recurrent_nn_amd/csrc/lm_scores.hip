@@ -99,11 +99,12 @@ struct Best {
     uint32_t *count;
     int top;
     uint64_t bound;         // what no longer counts: the last of `top` kept keys
-    uint32_t kept;
+    uint32_t kept;          // in order
+    uint32_t settled;       // of the list that stay if what is offered next does not fit
 
     __device__ void begin(uint64_t *l, uint64_t *s, uint32_t *c, int k)
     {
-        list = l, sorted = s, count = c, top = k, bound = 0, kept = 0;
+        list = l, sorted = s, count = c, top = k, bound = 0, kept = settled = 0;
         if (threadIdx.x == 0)
             *count = 0;
         __syncthreads();
@@ -133,8 +134,8 @@ struct Best {
                 ++at;
             }
     }
-    // How many have been offered in all since the last order(); the caller
-    // gives up on what did not fit with forget().
+    // How many the list has been offered, kept ones among them.  The caller either
+    // settles them, or gives up on what came since the last time with forget().
     __device__ __forceinline__ uint32_t offered()
     {
         __syncthreads();
@@ -142,10 +143,11 @@ struct Best {
         __syncthreads();
         return n;
     }
+    __device__ __forceinline__ void settle(uint32_t n) { settled = n; }
     __device__ void forget()
     {
         if (threadIdx.x == 0)
-            *count = kept;
+            *count = settled;
         __syncthreads();
     }
     // Each key's place is the number of larger ones.
@@ -161,7 +163,7 @@ struct Best {
                 sorted[place] = key;
         }
         __syncthreads();
-        kept = n < (uint32_t)top ? n : (uint32_t)top;
+        kept = settled = n < (uint32_t)top ? n : (uint32_t)top;
         if (threadIdx.x < kept)
             list[threadIdx.x] = sorted[threadIdx.x];
         if (threadIdx.x == 0)
@@ -403,8 +405,10 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
         const uint32_t item_packs = part_batches * U;
         const uint32_t packs = few ? n * item_packs : last - first;
         auto wanted = [&](float f) { return odd || f >= edge; };
-        if (few)
+        if (few) {
             best.offer(order_key(f_rest, whole * 8 + tid), tid < rest && wanted(f_rest));
+            best.settle(best.offered());
+        }
         for (uint32_t base = 0; base < packs; base += 256) {
             const uint32_t q = base + tid;
             bool on = q < packs;
@@ -440,6 +444,8 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
                 }
             } else if (n > kList / 2) {
                 best.order(n);
+            } else {
+                best.settle(n);
             }
         }
         best.order(best.offered());

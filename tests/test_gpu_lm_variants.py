@@ -163,6 +163,23 @@ def test_scores_of_equal_entries_over_segments():
     check_scores(y.to(BF16), torch.tensor([5, 5, 70000]), 5)
 
 
+@pytest.mark.parametrize("vocab,dtype", [(140001, F32), (300007, BF16)])
+def test_scores_of_long_rows_in_segments(vocab, dtype):
+    g = torch.Generator().manual_seed(vocab)
+    x = torch.randn(6, vocab, generator=g) * 3
+    x[0] = 0.5                              # equal over all segments
+    x[1, :] = -INF                          # two entries, in different segments
+    x[1, 17] = x[1, vocab - 2] = 1.0
+    x[2] = torch.linspace(-20, 20, vocab)   # the best ones all in the last segment
+    x[3, vocab // 2] = NAN
+    x[4, :vocab // 3] = -INF                # segments without an entry
+    x[5] = 0.0
+    x[5, 17516:] = 1.0                      # equal ones that begin shortly before a round of reads ends
+    tokens = torch.tensor([vocab - 1, vocab - 2, 5, vocab // 2, vocab - 1, 0])
+    check_scores(x.to(dtype), tokens, 33)
+    check_scores(x.to(dtype), tokens, 0)
+
+
 def test_the_plain_call_and_the_other_way_are_the_same():
     # a stream of the caller's goes through Python, no stream through the compiled binding
     r = Draw(31)
