@@ -119,9 +119,11 @@ template <class T, int K, int VEC> static int conv_go(const ConvArgs &a, hipStre
 {
     const uint64_t slots = (uint64_t)((a.d.dim + VEC - 1) / VEC);
     // runs of up to 32 steps (the K - 1 inputs before a run are read twice),
-    // shorter ones while the chip is not full
+    // shorter ones while the chip is not full; never less than K - 1, so that only
+    // the first run, which may replace the window in place, reads it
+    static_assert(K - 1 <= 8, "a run is as long as the window");
     uint64_t run_steps = 32;
-    while (run_steps > 4 && slots * (uint64_t)a.d.batch *
+    while (run_steps > 8 && slots * (uint64_t)a.d.batch *
                                 (((uint64_t)a.d.steps + run_steps - 1) / run_steps) < 262144)
         run_steps /= 2;
     uint64_t runs = ((uint64_t)a.d.steps + run_steps - 1) / run_steps;

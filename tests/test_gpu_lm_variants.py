@@ -139,6 +139,17 @@ def test_convolution_of_odd_channels_with_its_window_in_place():
             assert_close(hold, win, 0, "window")
 
 
+@pytest.mark.parametrize("steps", [5, 8, 9, 16, 40])
+def test_convolution_with_its_window_in_place_and_many_runs(steps):
+    r = Draw(steps)
+    x, w = r.normal(70, steps, 260).cuda(), r.normal(260, 8).cuda()
+    state = r.normal(70, 7, 260).cuda()
+    want, window = ra.causal_conv(x, w, state=state)
+    hold = state.clone()
+    got, _ = ra.causal_conv(x, w, state=hold, state_out=hold)
+    assert torch.equal(got, want) and torch.equal(hold, window)
+
+
 @pytest.mark.parametrize("rows,vocab,top,dtype", [
     (1, 262144, 64, F32), (1, 8193, 3, BF16), (2, 16391, 64, F16), (7, 65539, 1, BF16),
     (520, 9001, 20, F32), (3, 8, 8, F32), (3, 7, 2, BF16), (2, 2049, 64, F32)])
