@@ -87,6 +87,22 @@ template <class T> struct Words4 {
             return T::load((typename T::raw)(v % 2 ? w[v / 2] >> 16 : w[v / 2] & 0xFFFFu));
     }
     __device__ __forceinline__ void load(const typename T::raw *p) { __builtin_memcpy(w, p, sizeof(w)); }
+    // Without the first `n` (0 to 3; else as it is, or of no meaning).
+    __device__ __forceinline__ void drop(int n)
+    {
+        if constexpr (kWords == 4) {
+            const uint32_t a = w[1], b = w[2], c = w[3];
+            if (n > 0) {
+                w[0] = n == 1 ? a : n == 2 ? b : c;
+                w[1] = n == 1 ? b : c;
+                w[2] = c;
+            }
+        } else {
+            const uint64_t all = ((uint64_t)w[1] << 32 | w[0]) >> (n > 0 ? 16 * (n & 3) : 0);
+            w[0] = (uint32_t)all;
+            w[1] = (uint32_t)(all >> 32);
+        }
+    }
     __device__ __forceinline__ void set(int v, typename T::raw r)
     {
         if constexpr (kWords == 4)

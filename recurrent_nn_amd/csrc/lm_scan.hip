@@ -110,8 +110,6 @@ template <int L> __device__ __forceinline__ float group_sum(float v)
 // states divide by four.  64 tokens x 4096 x 16: 8.6 us, 4.2 TB/s.
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kFewSteps = 8;
-
 // FOURS: the states divide by four, so that a lane's are one load.
 template <class T, int L, bool FOURS>
 __global__ __launch_bounds__(256) void scan_steps_kernel(ScanArgs a, uint32_t row_blocks,
@@ -246,15 +244,18 @@ struct Spans {
 
 constexpr int kTile = 64;
 
-// WHOLE: 16 channels in every workgroup and states in whole sixteens, so that
-// four adjacent ones are one load.  Else elements beyond the last are loaded as
-// the last (no load depends on a condition: it would be waited for on the spot)
-// and left out of sums and stores.
-template <class T, int S, bool WHOLE, bool OUT>
+// FOURS: 16 channels or more and four states or more, so that four adjacent ones
+// are one load: a last workgroup of fewer channels begins earlier and stores its
+// own only; the last states are loaded from the fourth last one on, and moved.
+// Else elements beyond the last are loaded as the last.  (No load depends on a
+// condition: it would be waited for on the spot.)  What a workgroup computes for
+// the channels of the one before is dropped, whatever it found in a state that
+// the other may have replaced.  PAD: the states may not be whole sixteens; lanes
+// beyond them are left out of sums.
+template <class T, int S, bool FOURS, bool PAD, bool OUT>
 __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
 {
     using raw = typename T::raw;
-    constexpr bool PAD = !WHOLE;
     constexpr int TT = kTile;
     constexpr int SP = TT + 20;         // 4 x 4 channels of 16 steps over all banks
     constexpr int BP = TT + 4;          // 16 lanes' 16-byte reads over all banks
@@ -275,7 +276,8 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
     const uint32_t channels = 4 * four + in % wide, span = in / wide % sp.count;
     const int64_t b = (row + (uint64_t)four * (batch / 2 + 1)) % batch;
     const uint32_t g = channels / sp.per16, part = channels % sp.per16;
-    const int64_t c0 = (int64_t)g * sp.per + part * 16, c_end = (int64_t)(g + 1) * sp.per;
+    const int64_t own = (int64_t)g * sp.per + part * 16, c_end = (int64_t)(g + 1) * sp.per;
+    const int64_t c0 = FOURS && own + 16 > c_end ? c_end - 16 : own;
     const int64_t steps = a.d.steps, dim = a.d.dim;
     const int N = (int)a.d.states;
     const int64_t len = row_length(a.lens, b, steps);
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
         using P4 = Words4<T>;
         const int p = threadIdx.x - 256, ch = p % 4 * 4, t0 = p / 4;
         const int64_t c = c0 + ch;
-        auto channel = [&](int v) { return WHOLE || c + v < c_end ? c + v : c_end - 1; };
+        auto channel = [&](int v) { return FOURS || c + v < c_end ? c + v : c_end - 1; };
         float bias[4], D[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
@@ -323,7 +325,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
 
         auto four_channels = [&](const raw *row) {
             P4 f;
-            if (WHOLE) {
+            if (FOURS) {
                 f.load(row + c);
             } else {
 #pragma unroll
@@ -334,8 +336,8 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
         };
         auto four_states = [&](const raw *row, int s) {
             P4 f;
-            if (WHOLE) {
-                f.load(row + 16 * s + ch);
+            if (FOURS) {
+                f.load(row + (!PAD || 16 * s + ch <= N - 4 ? 16 * s + ch : N - 4));
             } else {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
@@ -360,6 +362,14 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
             }
         };
         auto prepare = [&](uint32_t k) {
+            if (FOURS && PAD)
+#pragma unroll
+                for (int n = 0; n < S; ++n) {
+                    const int by = 16 * n + ch - (N - 4);
+                    Br[n].drop(by);
+                    if (OUT)
+                        Cr[n].drop(by);
+                }
             float s[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v)
@@ -406,12 +416,12 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
             for (int v = 0; v < 4; ++v)
                 out.v[v] = T::store(f[v]);
             if (start + (int64_t)k * TT + t0 < end) {
-                if (WHOLE) {
+                if (FOURS && c >= own) {
                     store_pack<T, 4>(y, out);
                 } else {
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        if (c + v < c_end)
+                        if (c + v >= own && c + v < c_end)
                             y[v] = out.v[v];
                 }
             }
@@ -439,7 +449,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
             for (int64_t t = (end > start ? end : start) + t0; t < stop; t += 64)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    if (WHOLE || c + v < c_end)
+                    if (c + v >= own && c + v < c_end)
                         zeros[t * a.d.y_step_stride + v] = T::store(0.0f);
         return;
     }
@@ -447,7 +457,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
     // ---- the states
     const int lane = threadIdx.x % 16, ch = threadIdx.x / 16;
     const int64_t c = c0 + ch;
-    const bool on = c < c_end;
+    const bool on = c < c_end, stored = on && c >= own;
     float h[S], A[S], sums = 0.0f;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
@@ -461,7 +471,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
             float *first = mine + (int64_t)sp.count * dim * N;
             if (span == 0)
                 h[s] = OUT ? *first : a.state_in ? a.state_in[(b * dim + c) * N + n] : 0.0f;
-            if (!OUT && span == 0)
+            if (!OUT && span == 0 && stored)
                 *first = h[s];
             if (OUT && span > 0 && tiles > 0)
 #pragma unroll 8
@@ -548,7 +558,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
     }
     if (!OUT) {
         sums = group_sum<16>(sums);
-        if (on && lane == 0)
+        if (stored && lane == 0)
             sp.sum[(b * sp.count + span) * dim + c] = sums;
     }
     // The row's last span that has steps (the first one if none has) has its
@@ -557,7 +567,7 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanArgs a, Spans sp)
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int n = lane + 16 * s;
-        if (!on || (PAD && n >= N))
+        if (!stored || (PAD && n >= N))
             continue;
         if (!OUT)
             sp.state[((b * (sp.count + 1) + span) * dim + c) * N + n] = h[s];
@@ -578,8 +588,6 @@ static void spans_of(const rnn_scan_desc &d, Spans &sp)
     sp.groups16 = (uint32_t)groups16;
     sp.count = 1;
     sp.length = (d.steps + kTile - 1) / kTile * kTile;
-    if (d.steps <= kFewSteps)
-        return;
     int64_t count = 512 / (groups16 * d.batch);
     if (count > d.steps / 128)
         count = d.steps / 128;
@@ -598,24 +606,26 @@ size_t scan_workspace(const rnn_scan_desc &d)
     return (size_t)d.batch * d.dim * ((sp.count + 1) * d.states + sp.count) * 4;
 }
 
-template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp, hipStream_t s)
+template <class T, int S, bool FOURS, bool PAD>
+static int scan_passes(const ScanArgs &a, const Spans &sp, hipStream_t s)
 {
     const dim3 grid((uint32_t)(sp.groups16 * sp.count * a.d.batch)), block(512);
-    const bool whole = a.d.states % 16 == 0 && sp.per % 16 == 0;
     if (sp.count > 1) {
-        if (whole)
-            scan_kernel<T, S, true, false><<<grid, block, 0, s>>>(a, sp);
-        else
-            scan_kernel<T, S, false, false><<<grid, block, 0, s>>>(a, sp);
+        scan_kernel<T, S, FOURS, PAD, false><<<grid, block, 0, s>>>(a, sp);
         const int rc = (int)hipGetLastError();
         if (rc)
             return rc;
     }
-    if (whole)
-        scan_kernel<T, S, true, true><<<grid, block, 0, s>>>(a, sp);
-    else
-        scan_kernel<T, S, false, true><<<grid, block, 0, s>>>(a, sp);
+    scan_kernel<T, S, FOURS, PAD, true><<<grid, block, 0, s>>>(a, sp);
     return (int)hipGetLastError();
+}
+
+template <class T, int S> static int scan_go(const ScanArgs &a, const Spans &sp, hipStream_t s)
+{
+    if (sp.per < 16 || a.d.states < 4)
+        return scan_passes<T, S, false, true>(a, sp, s);
+    return a.d.states % 16 ? scan_passes<T, S, true, true>(a, sp, s)
+                           : scan_passes<T, S, true, false>(a, sp, s);
 }
 
 // No steps: the state is handed on.
@@ -649,9 +659,28 @@ template <class T, int L> static int steps_go(const ScanArgs &a, hipStream_t s)
     return (int)hipGetLastError();
 }
 
+// Steps up to which the states stay in scan_steps_kernel, by the workgroups that
+// scan_kernel would have: it spends about 1.6 us of a compute unit on starting
+// each, and with 2048 or more the other one's waves fill the chip.  States up to 8
+// leave half of scan_kernel's lanes idle.  In bf16 (scan_kernel, scan_steps_kernel):
+// 512 workgroups, 16 states, 12 steps 7.8, 7.8 us; 1024, 16 steps 9.8, 9.5 us;
+// 2048, 32 steps 18.2, 16.2 us and 48 steps 20, 27 us; 16384, 32 steps 123, 71 us;
+// 4096, 8 states, 64 steps 42, 37 us and 128 steps 59, 70 us.
+static int64_t few_steps(const rnn_scan_desc &d, const Spans &sp)
+{
+    const int64_t workgroups = (int64_t)sp.groups16 * d.batch;
+    if (workgroups < 1024)
+        return 8;
+    if (workgroups < 2048)
+        return 16;
+    return workgroups >= 4096 && d.states <= 8 ? 64 : 32;
+}
+
 template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
 {
-    if (a.d.steps <= kFewSteps) {
+    Spans sp{};
+    spans_of(a.d, sp);
+    if (a.d.steps <= few_steps(a.d, sp)) {
         if (a.d.states <= 4)
             return steps_go<T, 1>(a, s);
         if (a.d.states <= 8)
@@ -660,8 +689,6 @@ template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
             return steps_go<T, 4>(a, s);
         return a.d.states <= 32 ? steps_go<T, 8>(a, s) : steps_go<T, 16>(a, s);
     }
-    Spans sp{};
-    spans_of(a.d, sp);
     if ((__int128)sp.groups16 * sp.count * a.d.batch > 0x1fffffff)       // (four times it in 32 bits)
         return (int)hipErrorInvalidConfiguration;
     sp.state = (float *)a.workspace;

@@ -113,6 +113,39 @@ def test_scan_lengths_around_its_tiles(steps, states):
     assert_close(gh, h, herr, "state")
 
 
+# Channels of a group and states of which four adjacent ones are loaded at once,
+# where the last workgroup's and the last four are moved.
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("per,states", [(16, 4), (17, 5), (31, 6), (19, 7), (18, 18), (33, 35),
+                                        (47, 49), (20, 62), (15, 6), (17, 3)])
+def test_scan_of_odd_channels_and_states(per, states, dtype):
+    spec = (2, 150, 2 * per, states, 2, dtype, True, True, True, True, True, True)
+    v = scan_inputs(Draw(per + states), *spec)
+    v["lens"][0] = 150
+    y, err, h, herr = lm_ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["z"],
+                                  v["dt_bias"], True, v["state"], v["lens"])
+    got, gh = scan_call(v, True, pad=1)
+    assert_close(got, y, err, "y")
+    assert_close(gh, h, herr, "state")
+    hold = cuda(v["state"]).clone()
+    again, _ = scan_call(v, True, pad=1, state=hold, state_out=hold)
+    assert torch.equal(again, got) and torch.equal(hold, gh)
+
+
+# Many rows, short prompts: as the workgroups fill the chip, the states stay in
+# registers for more steps.  (A group of one channel each is a workgroup.)
+@pytest.mark.parametrize("batch,steps,states", [
+    (4, 16, 16), (4, 17, 13), (8, 32, 6), (8, 33, 6), (16, 64, 8), (16, 65, 8), (16, 40, 9)])
+def test_scan_of_many_short_rows(batch, steps, states):
+    spec = (batch, steps, 256, states, 256, F32, True, True, True, True, True, True)
+    v = scan_inputs(Draw(batch + steps), *spec)
+    y, err, h, herr = lm_ref.scan(v["x"], v["dt"], v["A"], v["B"], v["C"], v["D"], v["z"],
+                                  v["dt_bias"], True, v["state"], v["lens"])
+    got, gh = scan_call(v, True)
+    assert_close(got, y, err, "y")
+    assert_close(gh, h, herr, "state")
+
+
 @pytest.mark.parametrize("states", [16, 13, 40])
 def test_scan_infinities_keep_to_their_channel_and_time(states):
     spec = (1, 200, 48, states, 1, F32, True, True, True, True, True, False)
