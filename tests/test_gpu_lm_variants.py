@@ -207,6 +207,31 @@ def test_scores_of_equal_entries_over_segments():
     check_scores(y.to(BF16), torch.tensor([5, 5, 70000]), 5)
 
 
+@pytest.mark.parametrize("vocab", [1, 7, 8, 9, 65, 129, 500, 511, 512, 513, 1000, 1024, 1025, 2041,
+                                   2047, 2048, 2049])
+@pytest.mark.parametrize("top,dtype", [(0, F16), (1, F32), (20, BF16), (64, F16), (64, F32)])
+def test_scores_of_short_rows(vocab, top, dtype):
+    r = Draw(vocab + top)
+    x = r.normal(14, vocab, scale=3.0)
+    x[1] = 0.5                              # equal entries
+    x[2, vocab // 2:] = 7.0                 # the best ones equal, of the higher indices
+    x[3] = torch.linspace(-9, 9, vocab)
+    x[4] = torch.linspace(9, -9, vocab)
+    x[5] = -INF
+    x[6, ::2] = -INF
+    x[7, vocab // 3] = NAN
+    x[8] = NAN
+    x[9, vocab - 1] = INF
+    x[10] = torch.finfo(dtype).min
+    x[11] = 0.0
+    x[11, ::3] = -0.0
+    x[12] = x[12].round()                   # many equal ones
+    x[13] = 100.0 + 1e-4 * x[13]            # equal in their upper 16 bits
+    tokens = torch.randint(0, vocab, (14,), generator=r.g)
+    tokens[0], tokens[7] = vocab - 1, vocab // 3
+    check_scores(x.to(dtype), tokens, top, pad=1)
+
+
 @pytest.mark.parametrize("vocab,dtype", [(140001, F32), (300007, BF16)])
 def test_scores_of_long_rows_in_segments(vocab, dtype):
     g = torch.Generator().manual_seed(vocab)
