@@ -73,6 +73,21 @@ def test_rows_rounded_inside_are_the_rounded_rows(rows, cols, dtype):
     assert rows <= 2 or torch.isnan(got[2]).all()
 
 
+@pytest.mark.parametrize("cols", [1, 7, 16, 31, 127, 128, 129, 500, 512, 513, 2047, 2048, 2049, 8193,
+                                  32768, 32769, 70001])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_rounding_of_rows_of_every_length(cols, dtype):
+    r = Draw(cols)
+    x = r.normal(67, cols, dtype=dtype)
+    x[3] = 0
+    x[5, cols - 1], x[6, cols // 2] = NAN, -INF
+    x[7, cols - 1] = 100.0                  # the largest is the last one
+    want_q, want_scale = lm_ref.quantize(x)
+    got = ra.quantize_rows(inside(x, 1))
+    assert np.array_equal(got.q.cpu().numpy(), want_q)
+    assert np.array_equal(got.scale.cpu().numpy(), want_scale, equal_nan=True)
+
+
 SPANS = [  # batch, steps, dim, states, groups, dtype, softplus, bias, skip, gate, state, lens
     (1, 900, 16, 16, 1, F32, True, True, True, True, True, False),
     (3, 700, 20, 16, 1, F32, True, True, True, True, True, True),
