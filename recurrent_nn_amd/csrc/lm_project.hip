@@ -522,17 +522,25 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
         project_rows_kernel<T, NoSource><<<few, 256, 0, s>>>(g, nullptr, 0, cols);
         return (int)hipGetLastError();
     }
-    // The largest tiles that give most of the 256 compute units one.  The smallest
+    // The largest tiles that give most of the 256 compute units one; oblong ones
+    // only where they are all there at once (1024 x 8192 x 8192: 256 of 256 x 128 78 us,
+    // 128 x 128 85 us; 256 x 8192 x 8192: 256 of 128 x 64 34 us, 64 x 64 39 us; but
+    // 3388 x 896 x 2838: 322 of 256 x 128 27 us, 128 x 128 22 us).  The smallest
     // ones, if they are all there at once, with the columns divided among the
     // waves, a quarter of the steps (2238 rows x 6607 columns x 68 outputs: 14.7
     // us against 17.5; with more tiles than that its memory of LDS, one workgroup
     // a unit, costs more: 777 x 1500 x 2101 13.2 against 10.6).
     if (tiles(64, 64) > 0x7fffffff)
         return (int)hipErrorInvalidConfiguration;
+    auto one_each = [&](int64_t n) { return n >= 192 && n <= 256; };
     if (tiles(256, 256) >= 192)
         tiles_go<T, 256, 256, 2, 4, 1, 4>(g, s);
+    else if (one_each(tiles(256, 128)))
+        tiles_go<T, 256, 128, 4, 2, 1, 4>(g, s);
     else if (tiles(128, 128) >= 192)
         tiles_go<T, 128, 128, 2, 2, 1, 4>(g, s);
+    else if (one_each(tiles(128, 64)))
+        tiles_go<T, 128, 64, 2, 2, 1, 4>(g, s);
     else if (tiles(64, 64) > 256)
         tiles_go<T, 64, 64, 2, 2, 1, 4>(g, s);
     else

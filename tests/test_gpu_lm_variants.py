@@ -40,6 +40,13 @@ def test_projection_tiles(rows, cols, outs, dtype):
     assert_close(got, y, lm_ref.stored(y, 2 * (err + 2 * lm_ref.U * np.abs(y)), dtype), "y")
 
 
+@pytest.mark.parametrize("rows,cols,outs,dtype", [
+    (1700, 176, 3900, F32), (2040, 64, 4095, BF16), (1930, 1000, 3973, F16),    # 256 x 128
+    (500, 96, 3970, BF16), (385, 63, 4090, F32), (512, 1234, 3333, F16)])       # 128 x 64
+def test_projection_oblong_tiles(rows, cols, outs, dtype):
+    test_projection_tiles(rows, cols, outs, dtype)
+
+
 @pytest.mark.parametrize("rows", [1, 3, 16])
 def test_projection_of_few_rows_and_many_weights(rows):
     r = Draw(rows)
