@@ -462,6 +462,8 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
         keys[tid] = tid < best.kept ? sorted[tid] : 0;
 }
 
+constexpr uint32_t kMostSegments = 512;
+
 // The segments of a row together.
 template <class T> __global__ __launch_bounds__(256) void scores_join_kernel(ScoresArgs a,
                                                                            uint32_t segments)
@@ -475,11 +477,37 @@ template <class T> __global__ __launch_bounds__(256) void scores_join_kernel(Sco
     const Part *in = (const Part *)((const uint64_t *)a.workspace + (int64_t)gridDim.x * n_keys) +
                      row * segments;
     const Token tk = token_of<T>(a, row, (const typename T::raw *)a.logits + row * a.d.logits_stride);
+    // If `need` segments have j + 1 keys at or above a key each, and need (j + 1) >=
+    // top, then nothing below it counts.  With need about half of the segments,
+    // few more than `top` keys are left to order (32 segments' best 32: 6.0 us, all of
+    // them ordered 18 us; no gain for 128 keys or fewer).
+    __shared__ uint64_t ends[kMostSegments], least;
+    uint32_t j = 0;
+    while (j + 1 < top && (top + j) / (j + 1) > (segments + 1) / 2)
+        ++j;
+    const uint32_t need = (top + j) / (j + 1);
+    const bool many = n_keys > 128;
+    for (uint32_t i = threadIdx.x; i < segments && many; i += 256)
+        ends[i] = keys[i * top + j];
+    if (threadIdx.x == 0)
+        least = 0;
     Best best;
     best.begin(list, sorted, &count, (int)top);
+    if (many) {
+        for (uint32_t i = threadIdx.x; i < segments; i += 256) {
+            uint32_t above = 0;
+#pragma unroll 8
+            for (uint32_t k = 0; k < segments; ++k)
+                above += ends[k] > ends[i];
+            if (above + 1 == need)
+                least = ends[i];
+        }
+        __syncthreads();
+    }
     for (uint32_t base = 0; base < n_keys; base += 256) {
         const uint32_t q = base + threadIdx.x;
-        best.offer(q < n_keys ? keys[q] : 0, q < n_keys);
+        const uint64_t key = q < n_keys ? keys[q] : 0;
+        best.offer(key, key >= least);
         const uint32_t n = best.offered();
         if (n > kList - 256)
             best.order(n);
@@ -654,15 +682,18 @@ template <class T, int K> __global__ __launch_bounds__(256) void scores_short_ke
     }
 }
 
-// Segments of a row: as many as bring about 512 workgroups, of 8192 elements
-// or more each.
+// Segments of a row: as many as bring about kMostSegments workgroups, of 8192
+// elements or more each, if they save a workgroup more elements than a second
+// launch takes (64 rows of 24000 in three 13.4 us, in one 11.0 us; 130 rows of
+// 131072 in three 24.1 us, in one 26.1 us; 200 rows of 50000 in two 20.2 us, in one
+// 16.0 us).
 static uint32_t segments_of(const rnn_scores_desc &d, uint32_t &packs)
 {
     const int64_t all = (d.vocab + 7) / 8;
-    int64_t n = 512 / d.rows;
+    int64_t n = kMostSegments / d.rows;
     if (n > (all + 1023) / 1024)
         n = (all + 1023) / 1024;
-    if (n < 1)
+    if (n < 1 || all / n * (n - 1) < 32768 / 8)
         n = 1;
     packs = (uint32_t)((all + n - 1) / n);
     return (uint32_t)((all + packs - 1) / packs);
