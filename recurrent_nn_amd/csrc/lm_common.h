@@ -160,11 +160,15 @@ __device__ __forceinline__ float wave_sum(float v)
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Four values to four 8-bit integers in a word; a row without a factor (zero,
-// or not finite) is 0.  |x factor| <= 127 (1 + 2^-23): rounds to 127 at most.
+// or not finite) is 0.  |x factor| <= 127 (1 + 2^-23): rounds to 127 at most.  Added
+// to 1.5 2^23, whose last place is 1, the product is rounded to an integer (half
+// to even), and its two's complement is the sum's last bits.
 __device__ __forceinline__ uint32_t to_8bit(float a, float b, float c, float d, float factor)
 {
-    auto one = [&](float v) { return (uint32_t)(int32_t)__builtin_rintf(v * factor) & 0xFFu; };
-    return factor == 0.0f ? 0u : one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+    auto one = [&](float v) { return __float_as_uint(v * factor + 0x1.8p23f); };
+    const uint32_t low = __builtin_amdgcn_perm(one(b), one(a), 0x0C0C0400u);
+    const uint32_t high = __builtin_amdgcn_perm(one(d), one(c), 0x04000C0Cu);
+    return factor == 0.0f ? 0u : low | high;
 }
 template <class T> __device__ __forceinline__ uint2 pack_8bit(const Pack<T, 8> &p, float factor)
 {

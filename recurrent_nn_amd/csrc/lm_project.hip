@@ -6,7 +6,7 @@
 // tiles of x and w go to LDS by direct loads, 32x32x32 products, the scales in
 // the epilogue: 8192^3 in 487 us (2.26 POPS), 8192 x 2048 x 8192 in 160 to 170.
 // Few rows: bound by reading w once; it goes from memory to the matrix unit's
-// registers: 4 x 2048 x 8192 in 7.9 us.
+// registers: 4 x 2048 x 8192 in 7.6 us.
 #include <type_traits>
 #include <utility>
 
@@ -328,7 +328,9 @@ __global__ __launch_bounds__(256) void project_rows_kernel(ProjectGo g, const vo
     const int row_packs = steps * 16;
     typedef typename std::conditional<FUSED, FROM, BF16>::type X;
     Pack<X, 8> keep[KEEP];
-    auto row_of = [&](int j) { return ((int)threadIdx.x + 256 * j) / row_packs; };
+    // (a pack's number and row_packs are below 2^12: the quotient is right)
+    const float of_row = 1.0f / (float)row_packs;
+    auto row_of = [&](int j) { return (int)(((float)(threadIdx.x + 256 * j) + 0.5f) * of_row); };
     if constexpr (FUSED) {
         if (threadIdx.x < 16)
             row_max[threadIdx.x] = 0;

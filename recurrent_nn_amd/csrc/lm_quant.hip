@@ -6,7 +6,7 @@
 // its maximum and its rounding (up to 32 elements a thread; what is longer is
 // read again, from the L2).  4, 16 or 64 lanes take a short row, so that no
 // barrier is needed and lanes without elements are few; longer ones take a
-// workgroup.  8192 x 4096 in bf16: 18.3 us, 5.5 TB/s.
+// workgroup.  8192 x 4096 in bf16: 17.7 us, 5.7 TB/s.
 #include <type_traits>
 
 #include "lm_common.h"
