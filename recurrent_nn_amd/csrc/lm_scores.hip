@@ -230,7 +230,10 @@ __device__ __forceinline__ void put_scores(const ScoresArgs &a, int64_t row, con
 
 // One segment of a row: packs [first, last) of 8 elements.  A thread takes
 // every 256th pack, U at a time: the loads of a batch are in flight while the
-// one before is summed.
+// one before is summed.  Where a row of 16-bit elements begins between two words
+// (every other row of an odd vocabulary), packs begin with its second element,
+// and the first one is taken by itself: 1024 x 131073 in bf16 60 us (70 without), no
+// alternatives 53 (61).
 template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresArgs a,
                                                                       uint32_t segments,
                                                                       uint32_t segment_packs)
@@ -246,11 +249,14 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t row = blockIdx.x / segments;
     const uint32_t segment = blockIdx.x % segments;
-    const uint32_t V = (uint32_t)a.d.vocab, all = (V + 7) / 8;
+    const raw *row_at = (const raw *)a.logits + row * a.d.logits_stride;
+    const uint32_t skip = sizeof(raw) == 2 && ((uintptr_t)row_at & 2) ? 1 : 0;
+    const uint32_t V = (uint32_t)a.d.vocab - skip, all = (V + 7) / 8;
     const uint32_t first = segment * segment_packs;
     const uint32_t last = first + segment_packs < all ? first + segment_packs : all;
     const uint32_t whole = last < V / 8 ? last : V / 8;      // packs of all 8 elements end here
-    const raw *x = (const raw *)a.logits + row * a.d.logits_stride;
+    const raw *x = row_at + skip;
+    const bool head = skip && segment == 0;     // x[-1] is this segment's
     const uint32_t batches = whole > first ? (whole - first + BATCH - 1) / BATCH : 0;
     const uint32_t part_batches = (batches + PARTS - 1) / PARTS;
 
@@ -265,14 +271,15 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
     if (batches > 0)
         load(0);
 
-    const Token tk = token_of<T>(a, row, x);
+    const Token tk = token_of<T>(a, row, row_at);
     const float mine = tk.value;
+    const int64_t id = tk.id - skip;            // in x; the row's first element may be -1
     // What counts as before the token: in packs before the token's own
     // !(x <= lower), lower the next value below it; from its own on
     // !(x <= mine).  The own pack's equal entries before it are added after.
     // (-inf is preceded by everything of lower index; a NaN is counted below.)
     const bool unordered = mine != mine;
-    const uint32_t token_pack = tk.known ? (uint32_t)(tk.id / 8) : 0;
+    const uint32_t token_pack = tk.known && id > 0 ? (uint32_t)(id / 8) : 0;
     float lower = mine;
     {
         const uint32_t u = __float_as_uint(mine);
@@ -285,14 +292,13 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
     Part p{{kLowest, 0.0f, 0.0f}, 0};
     uint32_t before = 0;                        // of the wave
     float top_of_part = -__builtin_inff(), top_of_all = top_of_part;
-    auto one = [&](const float (&f)[8], uint32_t i) {
+    auto one = [&](const float (&f)[8], float edge) {
         const float pm = __builtin_fmaxf(
             __builtin_fmaxf(__builtin_fmaxf(f[0], f[1]), __builtin_fmaxf(f[2], f[3])),
             __builtin_fmaxf(__builtin_fmaxf(f[4], f[5]), __builtin_fmaxf(f[6], f[7])));
         top_of_part = __builtin_fmaxf(top_of_part, pm);
         if (pm > p.s.m + 8.0f)                  // rare after the first pack
             p.s.rebase(pm);
-        const float edge = i < token_pack ? lower : mine;
         float e[8];
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -330,9 +336,9 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
                 for (int v = 0; v < 8; ++v)
                     f[v] = beyond ? -__builtin_inff() : f[v];
                 // (they must not count as before a token)
-                one(f, beyond ? ~0u : i);
+                one(f, !beyond && i < token_pack ? lower : mine);
             } else {
-                one(f, i);
+                one(f, i < token_pack ? lower : mine);
             }
         }
         if (++in_part == part_batches || end) {
@@ -355,21 +361,35 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
         for (int v = 1; v < 8; ++v)
             f[v] = -__builtin_inff();
         f[0] = f_rest;
-        one(f, ~0u);
+        one(f, mine);
         top_of_all = __builtin_fmaxf(top_of_all, f_rest);
+    }
+    const float f_head = head && tid == 0 ? T::load(x[-1]) : -__builtin_inff();
+    if (wave == 0 && head) {
+        float f[8];
+#pragma unroll
+        for (int v = 1; v < 8; ++v)
+            f[v] = -__builtin_inff();
+        f[0] = f_head;
+        one(f, __builtin_inff());
+        top_of_all = __builtin_fmaxf(top_of_all, f_head);
     }
     if (lane == 0)
         p.before = before;
     if (tid == 0 && tk.known && token_pack >= first && token_pack < last)
-        for (uint32_t v = token_pack * 8; v < (uint32_t)tk.id; ++v)
+        for (int64_t v = token_pack * 8; v < id; ++v)
             p.before += T::load(x[v]) == mine;
+    if (tid == 0 && head && tk.known && id >= 0)
+        p.before += !(f_head <= lower);
     p = over_workgroup(p, parts);
     const bool odd = !(p.s.sum < __builtin_inff());     // NaN or infinite entries
     if (tk.known && (odd || unordered)) {               // count by the keys themselves
         const uint64_t mine_key = order_key(mine, (uint32_t)tk.id);
         Part q{{kLowest, 0.0f, 0.0f}, 0};
         for (uint32_t v = first * 8 + tid; v < V && v < last * 8; v += 256)
-            q.before += order_key(T::load(x[v]), v) > mine_key;
+            q.before += order_key(T::load(x[v]), v + skip) > mine_key;
+        if (tid == 0 && head)
+            q.before += order_key(f_head, 0) > mine_key;
         __syncthreads();
         p.before = over_workgroup(q, parts).before;
     }
@@ -405,10 +425,11 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
         const uint32_t item_packs = part_batches * U;
         const uint32_t packs = few ? n * item_packs : last - first;
         auto wanted = [&](float f) { return odd || f >= edge; };
-        if (few) {
-            best.offer(order_key(f_rest, whole * 8 + tid), tid < rest && wanted(f_rest));
-            best.settle(best.offered());
-        }
+        if (head)
+            best.offer(order_key(f_head, 0), tid == 0 && wanted(f_head));
+        if (few)
+            best.offer(order_key(f_rest, skip + whole * 8 + tid), tid < rest && wanted(f_rest));
+        best.settle(best.offered());
         for (uint32_t base = 0; base < packs; base += 256) {
             const uint32_t q = base + tid;
             bool on = q < packs;
@@ -426,7 +447,7 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
                 const float f = T::load(pk.v[v]);
-                keys[v] = order_key(f, 8 * i + v);
+                keys[v] = order_key(f, skip + 8 * i + v);
                 want |= (uint32_t)(on && 8 * i + v < V && wanted(f)) << v;
             }
             best.offer(keys, want);
@@ -436,7 +457,7 @@ template <class T> __global__ __launch_bounds__(256) void scores_kernel(ScoresAr
 #pragma unroll 1
                 for (int v = 0; v < 8; ++v) {
                     const float f = T::load(pk.v[0]);
-                    best.offer(order_key(f, 8 * i + v), on && 8 * i + v < V && wanted(f));
+                    best.offer(order_key(f, skip + 8 * i + v), on && 8 * i + v < V && wanted(f));
                     best.order(best.offered());
 #pragma unroll
                     for (int u = 0; u < 7; ++u)

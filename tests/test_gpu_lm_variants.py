@@ -254,6 +254,28 @@ def test_scores_of_short_rows(vocab, top, dtype):
     check_scores(x.to(dtype), tokens, top, pad=1)
 
 
+# Rows of an odd vocabulary follow each other: every other one begins between two
+# words, and its first element is taken by itself.
+@pytest.mark.parametrize("vocab", [2049, 2057, 4097, 8199, 33001, 70001])
+@pytest.mark.parametrize("dtype,top", [(BF16, 20), (F16, 1), (BF16, 0), (F16, 64)])
+def test_scores_of_rows_that_begin_between_words(vocab, dtype, top):
+    r = Draw(vocab + top)
+    x = r.normal(20, vocab, scale=3.0)
+    tokens = torch.randint(0, vocab, (20,), generator=r.g)
+    for i in range(2, 20, 2):               # the same in rows of both kinds
+        x[i], tokens[i] = x[i + 1], tokens[i + 1] = x[0], 0
+    x[2:4, 0] = 30.0                        # the first element is the best
+    x[4:6], tokens[4:6] = 0.25, 0           # equal entries
+    x[6:8], tokens[6:8] = 0.25, vocab - 1
+    x[8:10, 0], tokens[8:10] = NAN, 5
+    x[10:12, 0], x[10:12, 1], tokens[10:12] = INF, INF, 1
+    x[12:14], tokens[12:14] = -INF, 1
+    x[14:16, 1:], tokens[14:16] = -INF, 7   # only the first one is left
+    x[16:18], tokens[16:18] = x[16].sort().values, vocab - 1
+    x[18:, 0], x[18:, 1], x[18:, 2], tokens[18:] = 9.0, 9.0, 9.0, 1
+    check_scores(x.to(dtype), tokens, top)
+
+
 @pytest.mark.parametrize("vocab,dtype", [(140001, F32), (300007, BF16)])
 def test_scores_of_long_rows_in_segments(vocab, dtype):
     g = torch.Generator().manual_seed(vocab)
