@@ -60,14 +60,15 @@ struct Call {
     int64_t device;
     void *stream;
 
-    // A device tensor; null for None where that is allowed.
+    // A device tensor with memory of its own (a transform's wrapper has none);
+    // null for None where that is allowed.
     const at::Tensor *tensor(PyObject *o, bool optional = false) const
     {
         if (optional && o == Py_None)
             return nullptr;
         need(THPVariable_Check(o));
         const at::Tensor &t = THPVariable_Unpack(o);
-        need(t.is_cuda() && t.device().index() == device);
+        need(t.is_cuda() && t.device().index() == device && t.has_storage());
         return &t;
     }
     // A dense tensor of this type and shape.
@@ -112,11 +113,14 @@ PyObject *results(int status, std::initializer_list<at::Tensor> outs)
     return tuple;
 }
 
-template <class F> int without_gil(F &&f)
+// A C entry point called without the interpreter lock.  What can throw (a
+// tensor's pointer) is an argument, so it is over before the lock is given up;
+// the entry points themselves let no exception out.
+template <class F, class... A> int without_gil(F entry, A... args)
 {
     int status;
     Py_BEGIN_ALLOW_THREADS
-    status = f();
+    status = entry(args...);
     Py_END_ALLOW_THREADS
     return status;
 }
@@ -167,11 +171,10 @@ PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)
         const at::Tensor h = state_out ? *state_out : at::empty({b, k - 1, d}, x.options());
         const rnn_conv_desc desc{b, t, d, x.stride(0), x.stride(1), y.stride(0), y.stride(1),
                                  (int32_t)k, truth(a[3]), type};
-        const int status = without_gil([&] {
-            return lib.conv(&desc, c.stream, x.data_ptr(), (const float *)weight.data_ptr(),
-                            (const float *)ptr(bias), ptr(state), (const int32_t *)ptr(lens),
-                            y.data_ptr(), h.data_ptr());
-        });
+        const int status = without_gil(lib.conv, &desc, c.stream, x.data_ptr(),
+                                       (const float *)weight.data_ptr(), (const float *)ptr(bias),
+                                       ptr(state), (const int32_t *)ptr(lens), y.data_ptr(),
+                                       h.data_ptr());
         return results(status, {y, h});
     });
 }
@@ -212,13 +215,11 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (status != RNN_OK)
             return results(status, {});
         const at::Tensor ws = bytes(x, size);
-        status = without_gil([&] {
-            return lib.scan(&desc, c.stream, size ? ws.data_ptr() : nullptr, size, x.data_ptr(),
-                            dt.data_ptr(), (const float *)A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                            (const float *)ptr(D), ptr(z), (const float *)ptr(bias),
-                            (const float *)ptr(state), (const int32_t *)ptr(lens), y.data_ptr(),
-                            (float *)h.data_ptr());
-        });
+        status = without_gil(lib.scan, &desc, c.stream, size ? ws.data_ptr() : nullptr, size,
+                             x.data_ptr(), dt.data_ptr(), (const float *)A.data_ptr(), B.data_ptr(),
+                             C.data_ptr(), (const float *)ptr(D), ptr(z), (const float *)ptr(bias),
+                             (const float *)ptr(state), (const int32_t *)ptr(lens), y.data_ptr(),
+                             (float *)h.data_ptr());
         return results(status, {y, h});
     });
 }
@@ -234,10 +235,9 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
         const int64_t rows = x.size(0), cols = x.size(1), pitch = (cols + 127) / 128 * 128;
         const at::Tensor q = at::empty({rows, pitch}, x.options().dtype(at::kChar));
         const at::Tensor scale = at::empty({rows}, x.options().dtype(at::kFloat));
-        const int status = without_gil([&] {
-            return lib.quantize(c.stream, rows, cols, type, x.data_ptr(), x.stride(0),
-                                (int8_t *)q.data_ptr(), pitch, (float *)scale.data_ptr());
-        });
+        const int status = without_gil(lib.quantize, c.stream, rows, cols, type, x.data_ptr(),
+                                       x.stride(0), (int8_t *)q.data_ptr(), pitch,
+                                       (float *)scale.data_ptr());
         return results(status, {pitch == cols ? q : q.narrow(1, 0, cols), scale});
     });
 }
@@ -284,11 +284,9 @@ PyObject *project(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (status != RNN_OK)
             return results(status, {});
         const at::Tensor ws = bytes(x, size);
-        status = without_gil([&] {
-            return lib.project(&desc, c.stream, size ? ws.data_ptr() : nullptr, size, x.data_ptr(),
-                               (const float *)ptr(x_scale), (const int8_t *)w.data_ptr(),
-                               (const float *)w_scale.data_ptr(), (const float *)ptr(bias), y.data_ptr());
-        });
+        status = without_gil(lib.project, &desc, c.stream, size ? ws.data_ptr() : nullptr, size,
+                             x.data_ptr(), (const float *)ptr(x_scale), (const int8_t *)w.data_ptr(),
+                             (const float *)w_scale.data_ptr(), (const float *)ptr(bias), y.data_ptr());
         return results(status, {y});
     });
 }
@@ -322,12 +320,10 @@ PyObject *scores(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         const at::Tensor entropy = at::empty({rows}, real);
         const at::Tensor top_logprobs = at::empty({rows, top}, real), top_ids = at::empty({rows, top}, whole);
-        status = without_gil([&] {
-            return lib.scores(&desc, c.stream, size ? ws.data_ptr() : nullptr, size, x.data_ptr(),
-                              ptr(tokens), tokens ? (float *)logprob.data_ptr() : nullptr,
-                              (float *)entropy.data_ptr(), tokens ? (int32_t *)rank.data_ptr() : nullptr,
-                              (float *)top_logprobs.data_ptr(), (int32_t *)top_ids.data_ptr());
-        });
+        status = without_gil(lib.scores, &desc, c.stream, size ? ws.data_ptr() : nullptr, size,
+                             x.data_ptr(), ptr(tokens), tokens ? (float *)logprob.data_ptr() : nullptr,
+                             (float *)entropy.data_ptr(), tokens ? (int32_t *)rank.data_ptr() : nullptr,
+                             (float *)top_logprobs.data_ptr(), (int32_t *)top_ids.data_ptr());
         return results(status, {logprob, entropy, rank, top_logprobs, top_ids});
     });
 }
