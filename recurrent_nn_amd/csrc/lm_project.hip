@@ -24,7 +24,19 @@ struct ProjectGo {
     int64_t x_stride, w_stride, y_stride;
     int32_t rows, outs;
     int32_t k_end;          // columns, rounded up to 16 (the pitch of both sides reaches it)
+    int32_t x_end;          // columns of x that count: k_end where it has zeros past the last
 };
+
+// The first n (none below 1, all from 16) of 16 columns, zeros behind them.
+__device__ __forceinline__ v4i first_columns(v4i v, int n)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = n - 4 * i;
+        v[i] &= b >= 4 ? -1 : b > 0 ? (1 << 8 * b) - 1 : 0;
+    }
+    return v;
+}
 
 // ---------------------------------------------------------------------------
 // Many rows.  A workgroup has BM tokens x BN outputs, WM x WN waves, or WK of
@@ -167,7 +179,7 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void project_tiles_kernel(Projec
     };
     using Products = std::make_integer_sequence<int, TM * TN>;
 
-    const int steps = g.k_end / (KB * WK);      // whole ones
+    const int steps = g.x_end / (KB * WK);      // whole ones
 #pragma unroll
     for (int k = 0; k < BUFFERS; ++k)
         if (k < steps)
@@ -208,14 +220,15 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void project_tiles_kernel(Projec
         products(even);
         products(odd);
     }
-    if (g.k_end % (KB * WK)) {                  // the last columns, zeros behind them
+    if (g.x_end % (KB * WK)) {                  // the last columns, zeros behind them
         const int k0 = steps * (KB * WK);
         int8_t *X = lds + steps % BUFFERS * BUFFER, *W = X + WK * BM * KB;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < XP; ++i)
             *(v4i *)(X + (i * THREADS + tid) * 16) =
-                k0 + kx[i] < g.k_end ? *(const v4i *)(xp[i] + k0) : v4i{};
+                k0 + kx[i] < g.k_end ? first_columns(*(const v4i *)(xp[i] + k0), g.x_end - k0 - kx[i])
+                                     : v4i{};
 #pragma unroll
         for (int i = 0; i < WP; ++i)
             *(v4i *)(W + (i * THREADS + tid) * 16) =
@@ -418,8 +431,8 @@ __global__ __launch_bounds__(256) void project_rows_kernel(ProjectGo g, const vo
             for (int h = 0; h < 2; ++h) {
                 const int k = (s + 4 * i) * 128 + lane / 16 * 16 + 64 * h;
                 v4i b = FUSED ? *(const v4i *)(x + (s + 4 * i < steps ? k : 0)) : f.x[i][h];
-                if (FUSED ? s + 4 * i >= steps : (s + 4 * i + 1) * 128 > g.k_end)
-                    b = k < g.k_end ? b : v4i{};
+                if (FUSED ? s + 4 * i >= steps : (s + 4 * i + 1) * 128 > g.x_end)
+                    b = first_columns(b, g.x_end - k);
                 acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i][h], b, acc, 0, 0, 0);
             }
     };
@@ -565,6 +578,7 @@ int launch_project(const ProjectArgs &a, hipStream_t s)
     g.rows = (int32_t)a.d.rows;
     g.outs = (int32_t)a.d.outs;
     g.k_end = (int32_t)((a.d.cols + 15) / 16 * 16);
+    g.x_end = a.d.x_dtype == RNN_DTYPE_I8 ? (int32_t)a.d.cols : g.k_end;
     if (a.d.x_dtype != RNN_DTYPE_I8 && !fused(a.d)) {
         QuantizeArgs q{};
         q.rows = a.d.rows;

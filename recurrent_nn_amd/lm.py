@@ -305,9 +305,10 @@ def quant_project(x, w, w_scale, bias=None, x_scale=None, out_dtype: Optional[to
 
     w int8 with rows at multiples of 16 bytes and w_scale [outs] float32, as
     :func:`quantize_rows` gives them; x float32, bfloat16 or float16 (rounded
-    to 8 bits inside, one scale for each row), or int8 rows with x_scale.
-    bias [outs] float32.  y is in ``out_dtype`` (default: x's type, float32
-    for int8 rows).
+    to 8 bits inside, one scale for each row), or int8 rows at multiples of 16
+    bytes with x_scale [rows] float32.  8-bit rows may be columns of wider ones,
+    whatever those hold.  bias [outs] float32.  y is in ``out_dtype`` (default:
+    x's type, float32 for int8 rows).
     """
     if stream is None and getattr(x, "is_cuda", False):
         device = _device()
