@@ -420,9 +420,9 @@ typedef struct rnn_quant_desc {
 /*
  * rnn_quant_project -- y[i,o] = (sum_k qx[i,k] w[o,k]) * (x_scale[i] * w_scale[o])
  * + bias[o], the sum exact in 32-bit integers.  w is int8 [outs, w_stride]: base
- * and w_stride multiples of 16 bytes, every row readable up to w_stride (the
- * columns past `cols` may hold anything).  With x_dtype I8, x follows the same
- * rule and x_scale [rows] is required; else x_scale must be NULL.  bias [outs]
+ * and w_stride multiples of 16 bytes, every row readable up to `cols` rounded up
+ * to 16 (the columns past `cols` may hold anything).  With x_dtype I8, x follows
+ * the same rule and x_scale [rows] is required; else x_scale must be NULL.  bias [outs]
  * float32 may be NULL.
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
  *   strides or types outside their ranges, a missing or misaligned tensor, a

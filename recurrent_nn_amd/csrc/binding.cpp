@@ -242,13 +242,14 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     });
 }
 
-// 8-bit rows, readable up to their pitch.
+// 8-bit rows, readable in whole 16-byte pieces.
 void eight_bit(const at::Tensor &t)
 {
     need(t.scalar_type() == at::kChar && t.dim() == 2);
     Call::last_contiguous(t);
-    need(t.stride(0) == t.size(1) ||
-         (int64_t)t.storage().nbytes() >= t.storage_offset() + t.size(0) * t.stride(0));
+    need(t.size(0) == 0 || t.stride(0) == t.size(1) ||
+         (int64_t)t.storage().nbytes() >= t.storage_offset() + (t.size(0) - 1) * t.stride(0) +
+                                              (t.size(1) + 15) / 16 * 16);
 }
 
 // x, w, w_scale, bias, x_scale, out_dtype, out

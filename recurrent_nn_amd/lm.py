@@ -292,11 +292,13 @@ def _eight_bit(name, t, device):
 
 
 def _readable(name, t):
-    """The kernels read 8-bit rows up to their pitch, the last one too."""
-    pitch = t.stride(0)
-    if pitch != t.shape[1] and \
-            t.untyped_storage().nbytes() < t.storage_offset() + t.shape[0] * pitch:
-        raise ValueError(f"{name}: its last row must be readable up to the row pitch")
+    """The kernels read whole 16-byte pieces of 8-bit rows, also the last row's.
+    (A pitch of as many columns is a multiple of 16, or refused as it is.)"""
+    (rows, cols), pitch = t.shape, t.stride(0)
+    if rows > 0 and pitch != cols and \
+            t.untyped_storage().nbytes() < t.storage_offset() + (rows - 1) * pitch + (cols + 15) // 16 * 16:
+        raise ValueError(f"{name}: its last row must be readable up to a multiple of 16 columns "
+                         "(as within a row pitch of 16 bytes)")
 
 
 def quant_project(x, w, w_scale, bias=None, x_scale=None, out_dtype: Optional[torch.dtype] = None,

@@ -40,3 +40,30 @@ def test_columns_past_the_last_of_few_rows_and_many_weights():
     for cols in (4099, 4111, 4095):
         got = ra.quant_project(x[:, :cols], w[:, :cols], one, x_scale=one[:3])
         assert torch.equal(got, sums(x[:, :cols], w[:, :cols]))
+
+
+@pytest.mark.parametrize("lo,hi", [(1024, 2048), (0, 1024), (1936, 2048), (2032, 2041), (16, 1999)])
+@pytest.mark.parametrize("rows", [2, 40])
+def test_column_slices_of_weights_are_taken(rows, lo, hi):
+    r = Draw(rows + lo)
+    x = r.normal(rows, hi - lo).cuda()
+    w = torch.randint(-128, 128, (64, 2048), generator=r.g, dtype=torch.int8).cuda()
+    ws = r.uniform(64, lo=0.5, hi=1.5).cuda()
+    dense = torch.zeros(64, 2048, dtype=torch.int8, device="cuda")[:, :hi - lo]
+    dense.copy_(w[:, lo:hi])
+    want = ra.quant_project(x, dense, ws)
+    q = ra.quantize_rows(x)
+    wide = torch.ones(rows, 2048, dtype=torch.int8, device="cuda")
+    wide[:, lo:hi] = q.q
+    for stream in (None, torch.cuda.current_stream()):      # the compiled call, and the other way
+        assert torch.equal(ra.quant_project(x, w[:, lo:hi], ws, stream=stream), want)
+        assert torch.equal(ra.quant_project(wide[:, lo:hi], w[:, lo:hi], ws, x_scale=q.scale,
+                                            stream=stream), want)
+
+
+def test_rows_that_end_inside_a_piece_of_16_bytes_are_refused():
+    x, ws = torch.zeros(2, 8).cuda(), torch.ones(4).cuda()
+    w = torch.zeros(4 * 16 - 8, dtype=torch.int8).cuda().as_strided((4, 8), (16, 1))
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(ValueError, match="w: its last row"):
+            ra.quant_project(x, w, ws, stream=stream)

@@ -266,3 +266,18 @@ def test_reference_quantize():
     q, s = lm_ref.quantize(x)
     assert q[0].tolist() == [64, -127, 32] and s[0] == np.float32(2) / np.float32(127)
     assert not q[1:].any() and s[1] == 0 and np.isnan(s[2]) and np.isnan(s[3])
+
+
+def test_column_slices_of_8_bit_rows_are_readable():
+    from recurrent_nn_amd import lm
+    w = torch.zeros(64, 2048, dtype=torch.int8)
+    for lo, hi in ((0, 2048), (1024, 2048), (2032, 2048), (2032, 2047), (16, 17), (0, 1000)):
+        lm._readable("w", w[:, lo:hi])
+    lm._readable("w", w[:0, 16:])
+    dense = torch.zeros(4 * 16, dtype=torch.int8)
+    lm._readable("w", dense.as_strided((4, 8), (16, 1)))
+    for cut in (1, 8, 15):                  # the last row's piece of 16 bytes is cut off
+        with pytest.raises(ValueError, match="row pitch"):
+            lm._readable("w", dense[:-cut].clone().as_strided((4, 8), (16, 1), 0))
+    with pytest.raises(ValueError, match="w:"):
+        lm._readable("w", w.flatten()[:-9].clone().as_strided((64, 1999), (2048, 1), 40))
