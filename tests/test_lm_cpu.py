@@ -276,7 +276,7 @@ def test_column_slices_of_8_bit_rows_are_readable():
     lm._readable("w", w[:0, 16:])
     dense = torch.zeros(4 * 16, dtype=torch.int8)
     lm._readable("w", dense.as_strided((4, 8), (16, 1)))
-    for cut in (1, 8, 15):                  # the last row's piece of 16 bytes is cut off
+    for cut in (1, 5, 8):                   # the last row's piece of 16 bytes is cut off
         with pytest.raises(ValueError, match="row pitch"):
             lm._readable("w", dense[:-cut].clone().as_strided((4, 8), (16, 1), 0))
     with pytest.raises(ValueError, match="w:"):
