@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -60,8 +61,8 @@ struct Call {
     int64_t device;
     void *stream;
 
-    // A device tensor with memory of its own (a transform's wrapper has none);
-    // null for None where that is allowed.
+    // A device tensor with memory of its own (a transform's wrapper has none), of
+    // which no gradient is asked; null for None where that is allowed.
     const at::Tensor *tensor(PyObject *o, bool optional = false) const
     {
         if (optional && o == Py_None)
@@ -69,6 +70,7 @@ struct Call {
         need(THPVariable_Check(o));
         const at::Tensor &t = THPVariable_Unpack(o);
         need(t.is_cuda() && t.device().index() == device && t.has_storage());
+        need(!(t.requires_grad() && at::GradMode::is_enabled()));
         return &t;
     }
     // A dense tensor of this type and shape.

@@ -2,10 +2,12 @@
 binding of rnn_conv_run, rnn_scan_run, rnn_quantize_rows, rnn_quant_project
 and rnn_token_scores (include/recurrent_nn_amd.h has their definitions).
 
-Forward only: nothing is recorded for gradients.  Tensors live on one HIP device; the work goes to ``stream`` (default: torch's
-current stream of that device) and nothing waits for it.  What a call returns
-is new unless ``out`` / ``state_out`` supply it.  ValueError for tensors of
-the wrong kind, RNNError for what the library refuses.
+Forward only: nothing is recorded for gradients, and while they are recorded a
+tensor that requires one is refused (call under torch.no_grad(), or pass what
+detach() gives).  Tensors live on one HIP device; the work goes to ``stream``
+(default: torch's current stream of that device) and nothing waits for it.
+What a call returns is new unless ``out`` / ``state_out`` supply it.  ValueError
+for tensors of the wrong kind, RNNError for what the library refuses.
 
 A call on the current device's current stream, with every tensor as it should
 be, is checked and made by the compiled module _binding (csrc/binding.cpp) in
@@ -36,6 +38,14 @@ def _remember(key, value):
         _known.clear()
     _known[key] = value
     return value
+
+
+def _no_gradient(**tensors):
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} requires a gradient, and this operator has none: call it under "
+                                 "torch.no_grad(), or pass a detached tensor")
 
 
 def _sig(t):
@@ -155,6 +165,7 @@ def causal_conv(x, weight, bias=None, silu: bool = False, state=None, sequence_l
                                      device, _raw_stream(device))
         if r is not None:
             return _done(r, "rnn_conv_run")
+    _no_gradient(x=x, weight=weight, bias=bias, state=state, out=out, state_out=state_out)
     lib = _lib.load()
     key = ("conv", _sig(x), _sig(weight), _sig(bias), _sig(state), _sig(out), _sig(state_out), silu)
     known = _known.get(key)
@@ -209,6 +220,8 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
                                      out, state_out, device, _raw_stream(device))
         if r is not None:
             return _done(r, "rnn_scan_run")
+    _no_gradient(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, state=state, out=out,
+                 state_out=state_out)
     lib = _lib.load()
     key = ("scan", _sig(x), _sig(dt), _sig(A), _sig(B), _sig(C), _sig(D), _sig(z), _sig(dt_bias),
            _sig(state), _sig(out), _sig(state_out), dt_softplus)
@@ -269,6 +282,7 @@ def quantize_rows(x, stream=None) -> QuantRows:
         r = (_bound or _bind()).quantize(x, device, _raw_stream(device))
         if r is not None:
             return QuantRows._make(_done(r, "rnn_quantize_rows"))
+    _no_gradient(x=x)
     lib = _lib.load()
     _data("x", x, 2)
     rows, cols = x.shape
@@ -318,6 +332,7 @@ def quant_project(x, w, w_scale, bias=None, x_scale=None, out_dtype: Optional[to
                                         _raw_stream(device))
         if r is not None:
             return _done(r, "rnn_quant_project")[0]
+    _no_gradient(x=x, w_scale=w_scale, bias=bias, x_scale=x_scale, out=out)
     lib = _lib.load()
     key = ("project", _sig(x), _sig(w), _sig(w_scale), _sig(bias), _sig(x_scale), out_dtype, _sig(out))
     known = _known.get(key)
@@ -384,6 +399,7 @@ def token_scores(logits, tokens=None, top: int = 0, stream=None) -> TokenScores:
         r = (_bound or _bind()).scores(logits, tokens, top, device, _raw_stream(device))
         if r is not None:
             return TokenScores._make(_done(r, "rnn_token_scores"))
+    _no_gradient(logits=logits)
     lib = _lib.load()
     key = ("scores", _sig(logits), _sig(tokens), top)
     known = _known.get(key)
