@@ -309,6 +309,8 @@ void rnn_plan_destroy(rnn_plan *plan);
  *     overlap an input.
  *   - Sums, states and exponentials are float32 whatever the tensors' type, and
  *     rounded once (to nearest even) where a value is stored in fewer bits.
+ *   - A launch has fewer than 2^32 threads; what would need more is
+ *     RNN_ERR_UNSUPPORTED, and nothing is enqueued.
  *   - Every call is stream-ordered, allocates nothing and may be captured.
  *     Nothing is kept between calls.  Workspaces: device memory, 256-byte
  *     aligned, of at least the bytes that the matching *_workspace_size
@@ -348,7 +350,8 @@ typedef struct rnn_conv_desc {
  *   bias, state_in, sequence_lens, state_out may be NULL.
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, taps
  *   or dtype outside their ranges, a missing or misaligned tensor, y on x;
- *   RNN_ERR_UNSUPPORTED for 2^31 or more threads' worth of work.
+ *   RNN_ERR_UNSUPPORTED for 2^32 or more threads (one takes 8 bytes of channels,
+ *   or one channel, and 8 to 32 steps).
  */
 rnn_status rnn_conv_run(const rnn_conv_desc *desc, void *hip_stream, const void *x,
                         const float *weight, const float *bias, const void *state_in,
@@ -383,7 +386,9 @@ typedef struct rnn_scan_desc {
  *   states outside 1 to RNN_SCAN_MAX_STATES, groups that do not divide dim,
  *   an unknown dtype, a missing or misaligned tensor, y on an input, a
  *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for more
- *   than 2^31 - 1 channels or steps, or more workgroups than one launch takes.
+ *   than 2^31 - 1 channels or steps, or 2^32 or more threads: up to 8 to 64 steps
+ *   (by the sizes) a quarter of the states has one, beyond that 16 channels have
+ *   512 in each span of the steps.
  */
 rnn_status rnn_scan_workspace_size(const rnn_scan_desc *desc, size_t *bytes);
 rnn_status rnn_scan_run(const rnn_scan_desc *desc, void *hip_stream, void *workspace,
@@ -403,7 +408,8 @@ rnn_status rnn_scan_run(const rnn_scan_desc *desc, void *hip_stream, void *works
  *   channel), activations that several projections share once for each token.
  *   Errors: RNN_ERR_INVALID_INPUT for sizes below 0, strides or dtype outside
  *   their ranges, a missing or misaligned tensor; RNN_ERR_UNSUPPORTED for
- *   2^31 rows or more, or a q_stride above 2^30.
+ *   2^31 rows or more, a q_stride above 2^30, or 2^32 or more threads (4, 16, 64,
+ *   256 or 1024 a row: up to 128, 512, 2048, 32768 or more columns).
  */
 rnn_status rnn_quantize_rows(void *hip_stream, int64_t rows, int64_t cols, int32_t dtype,
                              const void *x, int64_t x_stride, int8_t *q, int64_t q_stride,
@@ -427,8 +433,9 @@ typedef struct rnn_quant_desc {
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
  *   strides or types outside their ranges, a missing or misaligned tensor, a
  *   workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED for cols
- *   above RNN_QUANT_MAX_COLS (beyond it a 32-bit sum can overflow) or for
- *   2^31 - 2^16 rows or outs or more.
+ *   above RNN_QUANT_MAX_COLS (beyond it a 32-bit sum can overflow), for
+ *   2^31 - 2^16 rows or outs or more, or for 2^32 or more threads (up to 16 rows,
+ *   16 an output; beyond that 512 a tile of 256 x 256; those of rnn_quantize_rows).
  */
 rnn_status rnn_quant_workspace_size(const rnn_quant_desc *desc, size_t *bytes);
 rnn_status rnn_quant_project(const rnn_quant_desc *desc, void *hip_stream, void *workspace,
@@ -459,7 +466,8 @@ typedef struct rnn_scores_desc {
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, top,
  *   dtype, token_bytes or stride outside their ranges, a missing or misaligned
  *   tensor, a workspace missing, too small or misaligned; RNN_ERR_UNSUPPORTED
- *   for 2^31 rows or a vocabulary of 2^31 - 2^16 or more.
+ *   for 2^31 rows, a vocabulary of 2^31 - 2^16 or more, or 2^32 or more threads
+ *   (64 a row up to 2048 entries, 256 beyond).
  */
 rnn_status rnn_scores_workspace_size(const rnn_scores_desc *desc, size_t *bytes);
 rnn_status rnn_token_scores(const rnn_scores_desc *desc, void *hip_stream, void *workspace,

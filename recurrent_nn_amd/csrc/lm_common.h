@@ -231,7 +231,11 @@ struct ScoresArgs {
     void *workspace;
 };
 
-// Each returns a hipError_t as int; sizes have been checked and are not zero.
+// Whether a launch can have so many workgroups: a grid's threads are counted in 32 bits.
+inline bool launchable(uint64_t workgroups, uint32_t threads) { return workgroups <= 0xFFFFFFFFu / threads; }
+
+// Each returns a hipError_t as int (hipErrorInvalidConfiguration, with nothing
+// enqueued, for more than a launch takes); sizes have been checked and are not zero.
 int launch_conv(const ConvArgs &a, hipStream_t s);
 size_t scan_workspace(const rnn_scan_desc &d);
 int launch_scan(const ScanArgs &a, hipStream_t s);

@@ -130,7 +130,7 @@ template <class T, int K, int VEC> static int conv_go(const ConvArgs &a, hipStre
     if (runs == 0)
         runs = 1;
     const uint64_t blocks = (slots * runs * (uint64_t)a.d.batch + 255) / 256;
-    if (blocks > 0x7fffffffull || runs > 0xffffffffull || slots > 0xffffffffull)
+    if (!launchable(blocks, 256) || runs > 0xffffffffull || slots > 0xffffffffull)
         return (int)hipErrorInvalidConfiguration;
     conv_kernel<T, K, VEC><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(
         a, (uint32_t)slots, (uint32_t)runs, (uint32_t)run_steps);

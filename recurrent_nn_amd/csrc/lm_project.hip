@@ -507,6 +507,22 @@ static void tiles_go(const ProjectGo &g, hipStream_t s)
         <<<dim3(m * n), dim3(64 * WM * WN * WK), 0, s>>>(g, m, n);
 }
 
+static int64_t tiles(const ProjectGo &g, int64_t bm, int64_t bn)
+{
+    return (g.rows + bm - 1) / bm * ((g.outs + bn - 1) / bn);
+}
+
+// Whether project_rows_kernel takes it.  Each of its workgroups reads all of x:
+// with 64 MiB of weights or more the tiles are faster for rows that are 8-bit
+// already, or that another launch rounds (16 rows x 8192 columns x 16384 outputs:
+// 22 us against 32; 8192 outputs of 2048 columns: 9.0 against 8.8 and no launch to
+// round).
+static bool by_rows(const ProjectGo &g, const rnn_quant_desc &d)
+{
+    const bool heavy = (int64_t)g.outs * g.k_end >= (int64_t)64 << 20 && tiles(g, 64, 64) >= 192;
+    return fused(d) || (g.rows <= kFewRows && d.cols > 0 && !heavy);
+}
+
 template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &a, hipStream_t s)
 {
     const dim3 few((uint32_t)((g.outs + (int64_t)15) / 16));
@@ -526,14 +542,7 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
         }
         return (int)hipGetLastError();
     }
-    auto tiles = [&](int64_t bm, int64_t bn) {
-        return (g.rows + bm - 1) / bm * ((g.outs + bn - 1) / bn);
-    };
-    // Each of its workgroups reads all of x: with 64 MiB of weights or more the
-    // tiles are faster (16 rows x 8192 columns x 16384 outputs: 22 us against
-    // 32; 8192 outputs of 2048 columns: 9.0 against 8.8 and no launch to round).
-    const bool heavy = (int64_t)g.outs * g.k_end >= (int64_t)64 << 20 && tiles(64, 64) >= 192;
-    if (g.rows <= kFewRows && cols > 0 && !heavy) {
+    if (by_rows(g, a.d)) {
         project_rows_kernel<T, NoSource><<<few, 256, 0, s>>>(g, nullptr, 0, cols);
         return (int)hipGetLastError();
     }
@@ -545,18 +554,16 @@ template <class T> static int project_go(const ProjectGo &g, const ProjectArgs &
     // waves, a quarter of the steps (2238 rows x 6607 columns x 68 outputs: 14.7
     // us against 17.5; with more tiles than that its memory of LDS, one workgroup
     // a unit, costs more: 777 x 1500 x 2101 13.2 against 10.6).
-    if (tiles(64, 64) > 0x7fffffff)
-        return (int)hipErrorInvalidConfiguration;
     auto one_each = [&](int64_t n) { return n >= 192 && n <= 256; };
-    if (tiles(256, 256) >= 192)
+    if (tiles(g, 256, 256) >= 192)
         tiles_go<T, 256, 256, 2, 4, 1, 4>(g, s);
-    else if (one_each(tiles(256, 128)))
+    else if (one_each(tiles(g, 256, 128)))
         tiles_go<T, 256, 128, 4, 2, 1, 4>(g, s);
-    else if (tiles(128, 128) >= 192)
+    else if (tiles(g, 128, 128) >= 192)
         tiles_go<T, 128, 128, 2, 2, 1, 4>(g, s);
-    else if (one_each(tiles(128, 64)))
+    else if (one_each(tiles(g, 128, 64)))
         tiles_go<T, 128, 64, 2, 2, 1, 4>(g, s);
-    else if (tiles(64, 64) > 256)
+    else if (tiles(g, 64, 64) > 256)
         tiles_go<T, 64, 64, 2, 2, 1, 4>(g, s);
     else
         tiles_go<T, 64, 64, 1, 1, 4, 3>(g, s);
@@ -579,6 +586,10 @@ int launch_project(const ProjectArgs &a, hipStream_t s)
     g.outs = (int32_t)a.d.outs;
     g.k_end = (int32_t)((a.d.cols + 15) / 16 * 16);
     g.x_end = a.d.x_dtype == RNN_DTYPE_I8 ? (int32_t)a.d.cols : g.k_end;
+    // (tiles smaller than the largest are a few thousand at most)
+    if (!(by_rows(g, a.d) ? launchable(((uint64_t)g.outs + 15) / 16, 256)
+                          : launchable((uint64_t)tiles(g, 256, 256), 512)))
+        return (int)hipErrorInvalidConfiguration;
     if (a.d.x_dtype != RNN_DTYPE_I8 && !fused(a.d)) {
         QuantizeArgs q{};
         q.rows = a.d.rows;

@@ -95,11 +95,14 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void quantize_kernel
         a.scale[row] = rs.scale;
 }
 
-template <class T, int THREADS> static void quantize_rows_go(const QuantizeArgs &a, hipStream_t s)
+template <class T, int THREADS> static int quantize_rows_go(const QuantizeArgs &a, hipStream_t s)
 {
     constexpr int ROWS = THREADS < 256 ? 256 / THREADS : 1;
-    quantize_kernel<T, THREADS>
-        <<<dim3((uint32_t)((a.rows + ROWS - 1) / ROWS)), dim3(THREADS * ROWS), 0, s>>>(a);
+    const int64_t blocks = (a.rows + ROWS - 1) / ROWS;
+    if (!launchable(blocks, THREADS * ROWS))
+        return (int)hipErrorInvalidConfiguration;
+    quantize_kernel<T, THREADS><<<dim3((uint32_t)blocks), dim3(THREADS * ROWS), 0, s>>>(a);
+    return (int)hipGetLastError();
 }
 
 // The fewest threads whose registers (32 elements each) hold a row: 100000 x 100
@@ -107,28 +110,24 @@ template <class T, int THREADS> static void quantize_rows_go(const QuantizeArgs 
 // a wave 10.2 us.  1024 threads only where they read ahead of the row's second
 // reading (300 x 100000: 23.5 us, 256 threads 45.5 us); 2000 x 9000 fits them and
 // takes 18.4 us, 256 threads 12.6 us.
-template <class T> static void quantize_go(const QuantizeArgs &a, hipStream_t s)
+template <class T> static int quantize_go(const QuantizeArgs &a, hipStream_t s)
 {
     if (a.cols <= 128)
-        quantize_rows_go<T, 4>(a, s);
-    else if (a.cols <= 512)
-        quantize_rows_go<T, 16>(a, s);
-    else if (a.cols <= 2048)
-        quantize_rows_go<T, 64>(a, s);
-    else if (a.cols <= 32768)
-        quantize_rows_go<T, 256>(a, s);
-    else
-        quantize_rows_go<T, 1024>(a, s);
+        return quantize_rows_go<T, 4>(a, s);
+    if (a.cols <= 512)
+        return quantize_rows_go<T, 16>(a, s);
+    if (a.cols <= 2048)
+        return quantize_rows_go<T, 64>(a, s);
+    return a.cols <= 32768 ? quantize_rows_go<T, 256>(a, s) : quantize_rows_go<T, 1024>(a, s);
 }
 
 int launch_quantize(const QuantizeArgs &a, hipStream_t s)
 {
     switch (a.dtype) {
-    case RNN_DTYPE_F32: quantize_go<F32>(a, s); break;
-    case RNN_DTYPE_BF16: quantize_go<BF16>(a, s); break;
-    default: quantize_go<F16>(a, s); break;
+    case RNN_DTYPE_F32: return quantize_go<F32>(a, s);
+    case RNN_DTYPE_BF16: return quantize_go<BF16>(a, s);
+    default: return quantize_go<F16>(a, s);
     }
-    return (int)hipGetLastError();
 }
 
 }  // namespace rnnamd

@@ -639,7 +639,7 @@ __global__ __launch_bounds__(256) void scan_no_steps_kernel(const float *in, flo
 static int no_steps_go(const ScanArgs &a, hipStream_t s)
 {
     const int64_t n = a.d.batch * a.d.dim * a.d.states;
-    if ((n + 255) / 256 > 0x7fffffff)
+    if (!launchable((uint64_t)(n + 255) / 256, 256))
         return (int)hipErrorInvalidConfiguration;
     scan_no_steps_kernel<<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a.state_in, a.state_out, n);
     return (int)hipGetLastError();
@@ -649,7 +649,7 @@ template <class T, int L> static int steps_go(const ScanArgs &a, hipStream_t s)
 {
     const uint32_t per = (uint32_t)(a.d.dim / a.d.groups);
     const int64_t row_blocks = (a.d.dim * L + 255) / 256;
-    if (row_blocks * a.d.batch > 0x7fffffff)
+    if (!launchable((uint64_t)(row_blocks * a.d.batch), 256))
         return (int)hipErrorInvalidConfiguration;
     const dim3 grid((uint32_t)(row_blocks * a.d.batch)), block(256);
     if (a.d.states % 4 == 0)
@@ -689,7 +689,8 @@ template <class T> static int scan_type(const ScanArgs &a, hipStream_t s)
             return steps_go<T, 4>(a, s);
         return a.d.states <= 32 ? steps_go<T, 8>(a, s) : steps_go<T, 16>(a, s);
     }
-    if ((__int128)sp.groups16 * sp.count * a.d.batch > 0x1fffffff)       // (four times it in 32 bits)
+    // (the kernel has four times their number in 32 bits)
+    if (!launchable((uint64_t)sp.groups16 * sp.count * a.d.batch, 512))
         return (int)hipErrorInvalidConfiguration;
     sp.state = (float *)a.workspace;
     sp.sum = sp.state + (size_t)a.d.batch * (sp.count + 1) * a.d.dim * a.d.states;

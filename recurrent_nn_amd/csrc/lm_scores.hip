@@ -741,6 +741,8 @@ size_t scores_workspace(const rnn_scores_desc &d)
 template <class T> static int scores_go(const ScoresArgs &a, hipStream_t s)
 {
     if (a.d.vocab <= kShortMost) {
+        if (!launchable((uint64_t)(a.d.rows + 3) / 4, 256))
+            return (int)hipErrorInvalidConfiguration;
         const dim3 grid((uint32_t)((a.d.rows + 3) / 4)), block(256);
         if (a.d.vocab <= 512)
             scores_short_kernel<T, 1><<<grid, block, 0, s>>>(a);
@@ -752,6 +754,8 @@ template <class T> static int scores_go(const ScoresArgs &a, hipStream_t s)
     }
     uint32_t packs;
     const uint32_t segments = segments_of(a.d, packs);
+    if (!launchable((uint64_t)a.d.rows * segments, 256))
+        return (int)hipErrorInvalidConfiguration;
     scores_kernel<T><<<dim3((uint32_t)a.d.rows * segments), dim3(256), 0, s>>>(a, segments, packs);
     const int rc = (int)hipGetLastError();
     if (rc || segments == 1)

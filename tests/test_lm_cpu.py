@@ -281,3 +281,31 @@ def test_column_slices_of_8_bit_rows_are_readable():
             lm._readable("w", dense[:-cut].clone().as_strided((4, 8), (16, 1), 0))
     with pytest.raises(ValueError, match="w:"):
         lm._readable("w", w.flatten()[:-9].clone().as_strided((64, 1999), (2048, 1), 40))
+
+
+def test_launches_of_too_many_threads_are_refused():
+    # (each of these is one more than a grid of 32 bits of threads takes, or a little more)
+    ws = (FAKE, 1 << 62)
+    one = dict(x_batch_stride=1, x_step_stride=1, y_batch_stride=1, y_step_stride=1)
+    assert conv(batch=1 << 32, steps=1, dim=1, **one) == UNSUPPORTED
+    assert ra.rnn_last_error() == "rnn_conv_run: more work than one launch takes"
+    wide = dict(groups=1, states=16, B_batch_stride=0, B_step_stride=0, C_batch_stride=0, C_step_stride=0,
+                x_batch_stride=0, x_step_stride=0, dt_batch_stride=0, dt_step_stride=0)
+    assert scan(ws=ws, batch=1 << 20, steps=1, dim=1024, y_batch_stride=1024, y_step_stride=1024,
+                **wide) == UNSUPPORTED
+    assert scan(ws=ws, batch=1 << 20, steps=65, dim=128, y_batch_stride=65 * 128, y_step_stride=128,
+                **wide) == UNSUPPORTED
+    assert scan(dict(state_out=FAKE), ws=ws, batch=1 << 20, steps=0, dim=512, **wide) == UNSUPPORTED
+    run = _lib.load().rnn_quantize_rows
+    for rows, cols in ((1 << 24, 2049), (1 << 24, 32768), (1 << 22, 32769), (1 << 26, 2048), (1 << 28, 500),
+                       (1 << 30, 100)):
+        pitch = (cols + 15) // 16 * 16
+        assert run(0, rows, cols, 1, FAKE, 0, 2 * FAKE, pitch, FAKE) == UNSUPPORTED, (rows, cols)
+    eight = dict(x_scale=FAKE)
+    for call, f in (({}, dict(rows=1, cols=16, outs=1 << 28, x_stride=16)),
+                    ({}, dict(rows=16, cols=1000, outs=1 << 28, x_stride=1008)),
+                    ({}, dict(rows=1 << 20, cols=16, outs=1 << 20, x_stride=16)),
+                    (eight, dict(rows=1 << 20, cols=16, outs=1 << 20, x_stride=16, x_dtype=3))):
+        assert project(call, ws=ws, w_stride=1008, y_stride=f["outs"], **f) == UNSUPPORTED, f
+    for rows, vocab in ((1 << 26, 8), (1 << 24, 4096)):
+        assert scores(ws=ws, rows=rows, vocab=vocab, logits_stride=0) == UNSUPPORTED
