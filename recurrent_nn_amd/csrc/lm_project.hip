@@ -225,10 +225,12 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void project_tiles_kernel(Projec
         int8_t *X = lds + steps % BUFFERS * BUFFER, *W = X + WK * BM * KB;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < XP; ++i)
-            *(v4i *)(X + (i * THREADS + tid) * 16) =
-                k0 + kx[i] < g.k_end ? first_columns(*(const v4i *)(xp[i] + k0), g.x_end - k0 - kx[i])
-                                     : v4i{};
+        for (int i = 0; i < XP; ++i) {
+            v4i v = k0 + kx[i] < g.k_end ? *(const v4i *)(xp[i] + k0) : v4i{};
+            if (g.x_end < g.k_end)
+                v = first_columns(v, g.x_end - k0 - kx[i]);
+            *(v4i *)(X + (i * THREADS + tid) * 16) = v;
+        }
 #pragma unroll
         for (int i = 0; i < WP; ++i)
             *(v4i *)(W + (i * THREADS + tid) * 16) =
