@@ -151,7 +151,13 @@ at::Tensor bytes(const at::Tensor &like, size_t n)
     return n ? at::empty({(int64_t)n}, like.options().dtype(at::kByte)) : at::Tensor();
 }
 
-bool truth(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();               // what it raised goes on
+    return v;
+}
 
 // x, weight, bias, silu, state, lens, out, state_out
 PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)

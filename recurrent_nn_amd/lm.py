@@ -167,6 +167,7 @@ def causal_conv(x, weight, bias=None, silu: bool = False, state=None, sequence_l
             return _done(r, "rnn_conv_run")
     _no_gradient(x=x, weight=weight, bias=bias, state=state, out=out, state_out=state_out)
     lib = _lib.load()
+    silu = bool(silu)
     key = ("conv", _sig(x), _sig(weight), _sig(bias), _sig(state), _sig(out), _sig(state_out), silu)
     known = _known.get(key)
     if known is None:
@@ -187,7 +188,7 @@ def causal_conv(x, weight, bias=None, silu: bool = False, state=None, sequence_l
         if out is not None:
             _expect("out", out, x.shape, x.dtype, x.device, dense=False)
             ys = out.stride()
-        desc = rnn_conv_desc(b, t, d, x.stride(0), x.stride(1), ys[0], ys[1], k, bool(silu),
+        desc = rnn_conv_desc(b, t, d, x.stride(0), x.stride(1), ys[0], ys[1], k, silu,
                              _DTYPES[x.dtype])
         known = _remember(key, (desc, ctypes.addressof(desc), (b, t, d), (b, k - 1, d)))
     _, desc, yshape, sshape = known
@@ -223,6 +224,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
     _no_gradient(x=x, dt=dt, A=A, B=B, C=C, D=D, z=z, dt_bias=dt_bias, state=state, out=out,
                  state_out=state_out)
     lib = _lib.load()
+    dt_softplus = bool(dt_softplus)
     key = ("scan", _sig(x), _sig(dt), _sig(A), _sig(B), _sig(C), _sig(D), _sig(z), _sig(dt_bias),
            _sig(state), _sig(out), _sig(state_out), dt_softplus)
     known = _known.get(key)
@@ -247,7 +249,7 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bo
         cs = C.stride() if C.dim() == 4 else (C.stride(0), C.stride(1), 0)
         desc = rnn_scan_desc(b, t, d, n, g, x.stride(0), x.stride(1), dt.stride(0), dt.stride(1),
                              zs[0], zs[1], ys[0], ys[1], bs[0], bs[1], bs[2], cs[0], cs[1], cs[2],
-                             _DTYPES[x.dtype], bool(dt_softplus))
+                             _DTYPES[x.dtype], dt_softplus)
         size = _workspace(lib.rnn_scan_workspace_size, desc)
         known = _remember(key, (desc, ctypes.addressof(desc), size, (b, t, d), (b, d, n)))
     _, desc, size, yshape, sshape = known

@@ -39,3 +39,24 @@ def test_every_entry_point_is_bound():
 def test_rows_too_long_are_refused():
     run = _lib.load().rnn_quantize_rows
     assert run(0, 1, 1 << 31, 0, 1 << 20, 1 << 31, 1 << 21, 1 << 31, 1 << 20) == ra.RNN_ERR_UNSUPPORTED
+
+
+def test_a_flag_without_a_truth_value_raises_what_it_says(compiled):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    class Neither:
+        def __bool__(self):
+            raise ArithmeticError("neither")
+
+    with FakeTensorMode():
+        def new(*shape):
+            return torch.empty(*shape, device="cuda")
+        x, B = new(2, 3, 8), new(2, 3, 4)
+        with pytest.raises(ArithmeticError, match="neither"):
+            compiled.conv(x, new(8, 4), None, Neither(), None, None, new(2, 3, 8), new(2, 3, 8), 0, 0)
+        with pytest.raises(ArithmeticError, match="neither"):
+            compiled.scan(x, x, new(8, 4), B, B, None, None, None, Neither(), None, None, new(2, 3, 8),
+                          new(2, 8, 4), 0, 0)
+    f = torch.zeros(2, 3, 8)
+    with pytest.raises(ArithmeticError, match="neither"):
+        ra.causal_conv(f, torch.zeros(8, 4), silu=Neither())
