@@ -81,9 +81,13 @@ STAMPS_BUILD = os.path.join(ROOT, "_build", "recurrent_nn_amd_stamps")
 STAMPS_LIB = os.path.join(HERE, "librecurrent_nn_amd_stamps.so")
 
 
-def build_binding(verbose: bool = False) -> str:
-    """The extension module recurrent_nn_amd._binding."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def build_binding(verbose: bool = False):
+    """The extension module recurrent_nn_amd._binding; None without torch, which
+    the library itself does not need."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared",
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
