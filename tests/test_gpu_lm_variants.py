@@ -326,3 +326,20 @@ def test_the_plain_call_and_the_other_way_are_the_same():
     with pytest.raises(ra.RNNError) as e:                # refused by the library in a compiled call
         ra.causal_conv(x, torch.zeros(48, 9).cuda())
     assert e.value.status == ra.RNN_ERR_INVALID_INPUT
+
+
+@pytest.mark.parametrize("rows,cols,outs", [(1, 8192, 16384), (1, 16000, 8200), (2, 8192, 9000), (4, 4096, 16400),
+                                            (16, 1024, 70000), (5, 8000, 9000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_other_types_beside_many_weights(rows, cols, outs, dtype):
+    # rounded inside up to 16384 elements, by a launch of its own beyond
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    x = torch.randn(rows, cols, generator=g, device="cuda").to(dtype)
+    w = torch.randint(-127, 128, (outs, cols), generator=g, device="cuda", dtype=torch.int8)
+    ws = torch.rand(outs, generator=g, device="cuda") + 0.5
+    q = ra.quantize_rows(x)
+    total = q.q.double() @ w.double().t().contiguous()          # exact
+    y = (total * q.scale.double()[:, None] * ws.double()).cpu().numpy()
+    got = ra.quant_project(x, w, ws)
+    assert_close(got, y, lm_ref.stored(y, 8 * lm_ref.U * np.abs(y), dtype), "y")
+    assert torch.equal(ra.quant_project(q.q, w, ws, x_scale=q.scale, out_dtype=dtype), got)
