@@ -8,7 +8,7 @@
 // stay in registers, so an input is loaded once by the run that owns it and
 // K - 1 times less by the next run (from the L2).  Eight bytes and not sixteen:
 // half the registers, twice the waves, and the loads of eight steps of each in
-// flight (8192 x 4096 in bf16: 27.5 us, 4.9 TB/s; with 16 bytes 37.4).
+// flight (8192 x 4096 in bf16: 28.2 us, 4.8 TB/s; with 16 bytes 37.4).
 #include "lm_common.h"
 
 namespace rnnamd {

@@ -4,7 +4,8 @@
 //
 // Many rows: bound by the matrix unit (and the clock, which falls under it);
 // tiles of x and w go to LDS by direct loads, 32x32x32 products, the scales in
-// the epilogue: 8192^3 in 487 us (2.26 POPS), 8192 x 2048 x 8192 in 160 to 170.
+// the epilogue: 8192^3 in 487 us (2.26 POPS), 8192 x 2048 x 8192 in 158 us once the
+// clock has settled (up to 190 in the first milliseconds of such work).
 // Few rows: bound by reading w once; it goes from memory to the matrix unit's
 // registers: 4 x 2048 x 8192 in 7.6 us.
 #include <type_traits>
@@ -44,11 +45,13 @@ __device__ __forceinline__ v4i first_columns(v4i v, int n)
 // part): a tile row is 64 bytes of LDS, whose 16-byte pieces are
 // permuted by the row (piece p of row r holds columns 16 (p xor r/4%4) on), so
 // that the sixteen rows that one pass of a 16-byte read takes (lanes 0-3, 12-15,
-// 20-23, 24-27, then the others) are in different banks.  The permutation is applied to the addresses that the direct loads
-// read from: in LDS they write in order.  Four buffers: three steps' loads are
-// in flight during the products of one, and a wave waits for its own part of
-// the next step only (by count), then for the others at the step's one barrier.
-// Operands are read half a step ahead, between the products of the half before.
+// 20-23, 24-27, then the others) are in different banks.  The permutation is applied
+// to the addresses that the direct loads read from: in LDS they write in order.
+// BUFFERS steps have a buffer each (four; three where the columns are divided): the
+// loads of BUFFERS - 1 steps are in flight during the products of one, and a wave
+// waits for its own part of the next step only (by count), then for the others at
+// the step's one barrier.  Operands are read half a step ahead, between the
+// products of the half before.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void load_to_lds(const int8_t *p, int8_t *lds)
@@ -184,9 +187,11 @@ __global__ __launch_bounds__(64 * WM * WN * WK) void project_tiles_kernel(Projec
     for (int k = 0; k < BUFFERS; ++k)
         if (k < steps)
             stage(k);
-    // Step k's loads have come for all waves: those of the BUFFERS - 2 steps after
-    // may be out.  The barrier also says that all have read step k - 1, whose
-    // buffer step k + BUFFERS - 1 gets.
+    // Step k, whose first half (even) has been read.  Before its barrier each wave has
+    // read the second half too and waited for that read (lgkmcnt) and for its own
+    // loads of step k + 1 (vmcnt; those of the BUFFERS - 2 steps after may be out).
+    // So after it step k + 1 is there for all, and nobody reads step k any more, whose
+    // buffer step k + BUFFERS gets: fetch(k, 1) has to stay above the wait.
     auto step = [&](int k, Half &even, Half &odd, auto more) {
         constexpr bool MORE = decltype(more)::value;
         fetch(k, 1, odd);

@@ -225,8 +225,9 @@ __global__ __launch_bounds__(256) void scan_steps_kernel(ScanArgs a, uint32_t ro
 //   h := exp(A sum s) h + h_span,  span by span,
 // and has all the outputs.
 //
-// 8192 steps x 4096 channels x 16 states in bf16: 190 us.  The vector unit is
-// busy 79% of the time, with ten instructions a step (of four channels): five on
+// 8192 steps x 4096 channels x 16 states in bf16: 191 us once the clock has settled
+// (216 to 235 in the first 20 ms from idle).  The vector unit is
+// busy 78% of the time, with ten instructions a step (of four channels): five on
 // the states, two for the sums, three of the preparing waves.  That is one
 // workgroup a compute unit; splitting the steps instead would compute e and u
 // twice.
