@@ -475,6 +475,153 @@ rnn_status rnn_token_scores(const rnn_scores_desc *desc, void *hip_stream, void 
                             float *logprob, float *entropy, int32_t *rank,
                             float *top_logprobs, int32_t *top_ids);
 
+/* ------------------------------------------------------------------------
+ * Operators of a delta-rule language model, and of decoding with several beams.
+ * The conventions of the section above hold here too.
+ * ---------------------------------------------------------------------- */
+
+#define RNN_DELTA_MAX_KEY_DIM 256
+#define RNN_DELTA_KEY_EPS 1e-6f
+#define RNN_BEAM_MAX 64
+#define RNN_REORDER_MAX_BEAMS 64
+
+/* q, k [batch, steps, key_heads, key_dim]; v, o [batch, steps, heads, value_dim];
+ * beta, g [batch, steps, heads] (heads contiguous); A, dt_bias [heads] float32;
+ * states [batch, heads, key_dim, value_dim] float32, dense. */
+typedef struct rnn_delta_desc {
+    int64_t batch, steps, key_heads, heads, key_dim, value_dim;
+                                       /* head j reads key head j / (heads / key_heads) */
+    int64_t q_batch_stride, q_step_stride, q_head_stride;
+    int64_t k_batch_stride, k_step_stride, k_head_stride;
+    int64_t v_batch_stride, v_step_stride, v_head_stride;
+    int64_t o_batch_stride, o_step_stride, o_head_stride;
+    int64_t beta_batch_stride, beta_step_stride;
+    int64_t g_batch_stride, g_step_stride;
+    int32_t dtype;                     /* of q, k, v and o: F32, BF16 or F16           */
+    int32_t gate_dtype;                /* of beta and g: F32 or dtype                  */
+    int32_t normalize;                 /* 1: q and k are divided by their norms        */
+    int32_t beta_sigmoid;              /* 1: b = 1 / (1 + exp(-beta))                  */
+    float scale;                       /* of the outputs                               */
+} rnn_delta_desc;
+
+/*
+ * rnn_delta_run -- gated delta rule.  Each head's state S [key_dim, value_dim]
+ * decays, is corrected towards v at the key k, and is read at the query q; for
+ * t = 0, 1, ...:
+ *     S = e^a S;   u = b (v - S^T k);   S = S + k u^T;   o = scale S^T q
+ * with b = beta[b,t,j] (through 1 / (1 + exp(-.)) with beta_sigmoid) and the
+ * logarithm of the decay a = g[b,t,j], or with A: a = A[j] log(1 + exp(g[b,t,j] +
+ * dt_bias[j])); without g: a = 0.  An a above 0 counts as 0, one below -104 (-inf
+ * too) as -104, where e^a is 0 in float32.  With `normalize`, q and k are divided
+ * by sqrt(sum x^2 + RNN_DELTA_KEY_EPS).  S = state_in (NULL = zeros) before the
+ * first step, state_out (nullable) = S after the last one.  One new token is a
+ * call with steps = 1.
+ *   Longer calls take their steps in chunks of 64, whose corrections solve a
+ *   triangular system: the same sums in another order.  A row's result does not
+ *   depend on the other rows, but the choice between chunks and single steps is
+ *   made for the whole call.
+ *   g, A (needs g), dt_bias (needs A), state_in, sequence_lens, state_out may be NULL.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
+ *   key_dim outside 1 to RNN_DELTA_MAX_KEY_DIM, key_heads that do not divide
+ *   heads, an unknown dtype, a scale that is not finite, a missing or misaligned
+ *   tensor, o on an input, a workspace missing, too small or misaligned;
+ *   RNN_ERR_UNSUPPORTED for 2^31 steps or more, or 2^32 or more threads (64 for 32
+ *   columns of a state; 256 for a head's chunk of 64 steps).
+ */
+rnn_status rnn_delta_workspace_size(const rnn_delta_desc *desc, size_t *bytes);
+rnn_status rnn_delta_run(const rnn_delta_desc *desc, void *hip_stream, void *workspace,
+                         size_t workspace_bytes, const void *q, const void *k, const void *v,
+                         const void *beta, const void *g, const float *A, const float *dt_bias,
+                         const float *state_in, const int32_t *sequence_lens, void *o,
+                         float *state_out);
+
+/* x, z, y [rows, groups, dim]; weight [dim], or [groups, dim] with
+ * weight_group_stride = dim, float32. */
+typedef struct rnn_norm_desc {
+    int64_t rows, groups, dim;
+    int64_t x_row_stride, x_group_stride;
+    int64_t z_row_stride, z_group_stride;
+    int64_t y_row_stride, y_group_stride;
+    int64_t weight_group_stride;       /* 0: all groups share it                       */
+    int32_t dtype;                     /* of x, z and y: F32, BF16 or F16              */
+    int32_t gate_first;                /* 1: x is gated before it is normed            */
+    float eps;                         /* 0 or more, finite                            */
+} rnn_norm_desc;
+
+/*
+ * rnn_gated_norm -- y = x / sqrt(mean x^2 + eps) * weight * z / (1 + exp(-z)), the
+ * mean over each group's dim elements; with gate_first the gate is a factor of x
+ * before the mean is taken; z may be NULL (no gate).  The sum of squares is
+ * float32: a group whose sum overflows it (values about 1e19) gives zeros.
+ * y may be x or z where strides agree (in place).
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, dtype,
+ *   eps or strides outside their ranges, gate_first without z, a missing or
+ *   misaligned tensor; RNN_ERR_UNSUPPORTED for a dim of 2^30 or more, or 2^32 or
+ *   more threads (4, 16, 64, 256 or 1024 a group: up to 64, 256, 2048, 16384 or
+ *   more elements).
+ */
+rnn_status rnn_gated_norm(const rnn_norm_desc *desc, void *hip_stream, const void *x,
+                          const float *weight, const void *z, void *y);
+
+typedef struct rnn_beam_desc {
+    int64_t batch, beams, vocab;       /* logits [batch, beams, vocab]                 */
+    int64_t logits_batch_stride, logits_beam_stride;
+    int32_t dtype;                     /* of the logits: F32, BF16 or F16              */
+    int32_t keep;                      /* candidates selected, 1 to RNN_BEAM_MAX       */
+    int64_t eos;                       /* the token of a finished beam                 */
+} rnn_beam_desc;
+
+/*
+ * rnn_beam_select -- one step of beam search.  Candidate (i, t) of a request
+ * continues beam i with token t and has the value
+ *     scores[b,i] + log(exp(x[b,i,t]) / sum_u exp(x[b,i,u]));
+ * the first `keep` in decreasing order of the value, equal ones in increasing
+ * order of i vocab + t, are written as out_scores, out_tokens and out_parents
+ * [batch, keep].  The normalisers are summed, and candidates of unlike beams
+ * compared, in float64.
+ *   finished (uint8 [batch, beams], nullable): a finished beam (not 0) is not
+ *   continued; its candidate (i, eos) has the value scores[b,i] and its others
+ *   -inf; its logits are not read.  A beam with a score that is not finite, or
+ *   whose logits are all -inf or hold +inf or NaN, has candidates of value -inf
+ *   only.  Where there are fewer than `keep` candidates, the rest has the score
+ *   -inf and token and parent -1.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, beams
+ *   outside 1 to RNN_BEAM_MAX, keep, dtype or strides outside their ranges, eos
+ *   outside [0, vocab) with `finished`, a missing or misaligned tensor, a workspace
+ *   missing, too small or misaligned; RNN_ERR_UNSUPPORTED for a vocabulary of
+ *   2^31 - 2^16 or more, or 2^32 or more threads (256 a beam).
+ */
+rnn_status rnn_beam_workspace_size(const rnn_beam_desc *desc, size_t *bytes);
+rnn_status rnn_beam_select(const rnn_beam_desc *desc, void *hip_stream, void *workspace,
+                           size_t workspace_bytes, const void *logits, const float *scores,
+                           const uint8_t *finished, float *out_scores, int32_t *out_tokens,
+                           int32_t *out_parents);
+
+/* A state tensor [outer, batch * beams, inner bytes], dense, and where its
+ * reordered form [outer, batch * keep, inner bytes] goes. */
+typedef struct rnn_reorder_item {
+    const void *in;
+    void *out;
+    int64_t outer, inner_bytes;
+} rnn_reorder_item;
+
+/*
+ * rnn_reorder_states -- row (b, j) of each of `count` tensors' reordered form is
+ * row (b, parents[b, j]) of the tensor.  parents is a DEVICE int32 array [batch,
+ * keep]; values outside [0, beams) are taken as the nearest of the two ends.  An
+ * item whose out is its in is reordered in place (keep = beams up to
+ * RNN_REORDER_MAX_BEAMS): only rows that change are read and written.
+ *   Any alignment of the tensors.  `items` is a HOST array, read during the call.
+ *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, a
+ *   missing tensor, an item whose out overlaps its in otherwise, in place with
+ *   keep other than beams; RNN_ERR_UNSUPPORTED for more than RNN_REORDER_MAX_BEAMS
+ *   beams in place, or 2^32 or more threads for 32 items (one for 16 bytes of
+ *   `beams` rows).
+ */
+rnn_status rnn_reorder_states(void *hip_stream, int64_t batch, int64_t beams, int64_t keep,
+                              const int32_t *parents, const rnn_reorder_item *items,
+                              int64_t count);
+
 /* Thread-local text describing the last non-OK status on this thread. */
 const char *rnn_last_error(void);
 

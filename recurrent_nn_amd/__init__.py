@@ -8,7 +8,9 @@ operator runs in the HIP library; if the library is missing, nothing runs.
 
 The operators of a selective-state language model (causal_conv,
 selective_scan, quantize_rows, quant_project, token_scores) are in
-:mod:`recurrent_nn_amd.lm` and reached from here; that module imports torch.
+:mod:`recurrent_nn_amd.lm`, those of a delta-rule language model and of decoding
+with several beams (gated_delta, gated_norm, beam_select, reorder_states) in
+:mod:`recurrent_nn_amd.delta`; they are reached from here, and import torch.
 """
 from __future__ import annotations
 
@@ -25,13 +27,19 @@ from ._lib import (RNN_OK, RNN_ERR_INVALID_INPUT, RNN_ERR_UNSUPPORTED, RNN_ERR_D
 
 LM_NAMES = ("causal_conv", "selective_scan", "quantize_rows", "quant_project", "token_scores",
             "QuantRows", "TokenScores")
+DELTA_NAMES = ("gated_delta", "gated_norm", "beam_select", "reorder_states", "BeamChoice")
 
 
 def __getattr__(name):
-    if name not in LM_NAMES:
+    if name in LM_NAMES:
+        from . import lm as module
+        names = LM_NAMES
+    elif name in DELTA_NAMES:
+        from . import delta as module
+        names = DELTA_NAMES
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import lm
-    globals().update((n, getattr(lm, n)) for n in LM_NAMES)
+    globals().update((n, getattr(module, n)) for n in names)
     return globals()[name]
 
 

@@ -28,6 +28,8 @@ EXPORTED = ["rnn_plan_create", "rnn_plan_workspace_size", "rnn_run", "rnn_cell_r
             "rnn_run_noalloc", "rnn_workspace_check",
             "rnn_plan_enable_timing", "rnn_plan_last_timings", "rnn_plan_describe",
             "rnn_plan_destroy", "rnn_last_error",
+            "rnn_delta_workspace_size", "rnn_delta_run", "rnn_gated_norm",
+            "rnn_beam_workspace_size", "rnn_beam_select", "rnn_reorder_states",
             "rnn_conv_run", "rnn_scan_workspace_size", "rnn_scan_run", "rnn_quantize_rows",
             "rnn_quant_workspace_size", "rnn_quant_project", "rnn_scores_workspace_size",
             "rnn_token_scores"]
@@ -37,6 +39,9 @@ RNN_CONV_MAX_TAPS = 8
 RNN_SCAN_MAX_STATES = 64
 RNN_QUANT_MAX_COLS = 131071
 RNN_SCORES_MAX_TOP = 64
+RNN_DELTA_MAX_KEY_DIM = 256
+RNN_BEAM_MAX = 64
+RNN_REORDER_MAX_BEAMS = 64
 
 
 class rnn_attrs(ctypes.Structure):
@@ -79,11 +84,14 @@ class rnn_dims(ctypes.Structure):
     ]
 
 
-def _struct(name, longs, ints):
-    """A descriptor: int64 fields, then int32 fields."""
+def _struct(name, longs, ints, floats="", last=""):
+    """A descriptor: int64 fields, then int32 fields, float fields, and int64
+    fields again."""
     return type(name, (ctypes.Structure,), {
         "_fields_": [(f, ctypes.c_int64) for f in longs.split()] +
-                    [(f, ctypes.c_int32) for f in ints.split()]})
+                    [(f, ctypes.c_int32) for f in ints.split()] +
+                    [(f, ctypes.c_float) for f in floats.split()] +
+                    [(f, ctypes.c_int64) for f in last.split()]})
 
 
 rnn_conv_desc = _struct(
@@ -98,6 +106,21 @@ rnn_quant_desc = _struct(
     "rnn_quant_desc", "rows cols outs x_stride w_stride y_stride", "x_dtype y_dtype")
 rnn_scores_desc = _struct(
     "rnn_scores_desc", "rows vocab logits_stride", "dtype token_bytes top")
+rnn_delta_desc = _struct(
+    "rnn_delta_desc", "batch steps key_heads heads key_dim value_dim q_batch_stride q_step_stride "
+    "q_head_stride k_batch_stride k_step_stride k_head_stride v_batch_stride v_step_stride "
+    "v_head_stride o_batch_stride o_step_stride o_head_stride beta_batch_stride beta_step_stride "
+    "g_batch_stride g_step_stride", "dtype gate_dtype normalize beta_sigmoid", "scale")
+rnn_norm_desc = _struct(
+    "rnn_norm_desc", "rows groups dim x_row_stride x_group_stride z_row_stride z_group_stride "
+    "y_row_stride y_group_stride weight_group_stride", "dtype gate_first", "eps")
+rnn_beam_desc = _struct(
+    "rnn_beam_desc", "batch beams vocab logits_batch_stride logits_beam_stride", "dtype keep", "", "eos")
+
+
+class rnn_reorder_item(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("outer", ctypes.c_int64), ("inner_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -149,7 +172,13 @@ def load() -> ctypes.CDLL:
     L.rnn_quant_project.argtypes = [vp, vp, vp, sz] + [vp] * 6
     L.rnn_scores_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
     L.rnn_token_scores.argtypes = [vp, vp, vp, sz] + [vp] * 7
-    for name in EXPORTED[-8:]:
+    L.rnn_delta_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    L.rnn_delta_run.argtypes = [vp, vp, vp, sz] + [vp] * 11
+    L.rnn_gated_norm.argtypes = [vp] * 6
+    L.rnn_beam_workspace_size.argtypes = [vp, ctypes.POINTER(sz)]
+    L.rnn_beam_select.argtypes = [vp, vp, vp, sz] + [vp] * 6
+    L.rnn_reorder_states.argtypes = [vp, i64, i64, i64, vp, vp, i64]
+    for name in EXPORTED[11:]:
         getattr(L, name).restype = i32
     _lib = L
     return L

@@ -5,7 +5,7 @@ Every HIP source is compiled by hipcc for --offload-arch=gfx950 with
 and with the packed-fp32 instructions disabled; the host-only plan code is
 plain C++17.  Objects go to _build/ (not versioned), the library next to this
 file, where the Python binding loads it.  The compiled part of the torch
-binding (csrc/binding.cpp: host code, on torch's own headers) is an extension
+binding (csrc/binding*.cpp: host code, on torch's own headers) is an extension
 module beside it.
 """
 import concurrent.futures as cf
@@ -53,7 +53,7 @@ HIP_UNITS = ([(f, [], f + ".o") for f in sorted(os.listdir(CSRC))
               if f.endswith(".hip") and f != INST] +
              [(INST, [f"-DRNN_FAMILY={fam}", f"-DRNN_ACT={act}", *FAMILY_FLAGS.get(fam, [])],
                f"recurrence_inst_f{fam}_a{act}.o") for fam, act in INST_UNITS] +
-             [("run.cpp", [], "run.cpp.o"), ("lm_run.cpp", [], "lm_run.cpp.o")])
+             [(f, [], f + ".o") for f in ("run.cpp", "lm_run.cpp", "lm_run_delta.cpp")])
 CXX_UNITS = [("plan.cpp", [], "plan.cpp.o")]
 BINDING = os.path.join(HERE, "_binding.so")
 
@@ -92,7 +92,7 @@ def build_binding(verbose: bool = False):
     cmd = ["g++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared",
            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-           os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           os.path.join(CSRC, "binding.cpp"), os.path.join(CSRC, "binding_delta.cpp"), "-o", tmp,
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)

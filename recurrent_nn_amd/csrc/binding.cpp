@@ -9,18 +9,7 @@
 // on another device than the current one) it returns None and does nothing:
 // the caller then does the same steps itself, and says what is wrong.  Returns
 // the outputs as a tuple, or the C status where that is not RNN_OK.
-#include <Python.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/core/grad_mode.h>
-#include <ATen/ops/empty.h>
-#include <torch/csrc/Dtype.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <initializer_list>
-
-#include "../../include/recurrent_nn_amd.h"
+#include "binding_common.h"
 
 namespace {
 
@@ -35,129 +24,6 @@ struct Entries {
     decltype(&rnn_scores_workspace_size) scores_size;
     decltype(&rnn_token_scores) scores;
 } lib;
-
-// What a check throws: this call is not one of the plain ones.
-struct NotPlain {};
-
-void need(bool ok)
-{
-    if (!ok)
-        throw NotPlain{};
-}
-
-int32_t type_of(at::ScalarType t)
-{
-    switch (t) {
-    case at::kFloat: return RNN_DTYPE_F32;
-    case at::kBFloat16: return RNN_DTYPE_BF16;
-    case at::kHalf: return RNN_DTYPE_F16;
-    default: throw NotPlain{};
-    }
-}
-
-using Sizes = std::initializer_list<int64_t>;
-
-struct Call {
-    int64_t device;
-    void *stream;
-
-    // A device tensor with memory of its own (a transform's wrapper has none), of
-    // which no gradient is asked; null for None where that is allowed.
-    const at::Tensor *tensor(PyObject *o, bool optional = false) const
-    {
-        if (optional && o == Py_None)
-            return nullptr;
-        need(THPVariable_Check(o));
-        const at::Tensor &t = THPVariable_Unpack(o);
-        need(t.is_cuda() && t.device().index() == device && t.has_storage());
-        need(!(t.requires_grad() && at::GradMode::is_enabled()));
-        return &t;
-    }
-    // A dense tensor of this type and shape.
-    const at::Tensor *dense(PyObject *o, at::ScalarType type, Sizes sizes, bool optional = true) const
-    {
-        const at::Tensor *t = tensor(o, optional);
-        if (t)
-            need(t->scalar_type() == type && t->sizes() == at::IntArrayRef(sizes) && t->is_contiguous());
-        return t;
-    }
-    // One whose last dimension is contiguous.
-    const at::Tensor *rows(PyObject *o, at::ScalarType type, at::IntArrayRef sizes, bool optional) const
-    {
-        const at::Tensor *t = tensor(o, optional);
-        if (t) {
-            need(t->scalar_type() == type && t->sizes() == sizes);
-            last_contiguous(*t);
-        }
-        return t;
-    }
-    static void last_contiguous(const at::Tensor &t) { need(t.size(-1) <= 1 || t.stride(-1) == 1); }
-};
-
-void *ptr(const at::Tensor *t) { return t ? t->data_ptr() : nullptr; }
-
-PyObject *results(int status, std::initializer_list<at::Tensor> outs)
-{
-    if (status != RNN_OK)
-        return PyLong_FromLong(status);
-    PyObject *tuple = PyTuple_New((Py_ssize_t)outs.size());
-    if (!tuple)
-        return nullptr;
-    Py_ssize_t i = 0;
-    for (const at::Tensor &t : outs) {
-        PyObject *o = t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
-        if (!o) {
-            Py_DECREF(tuple);
-            return nullptr;
-        }
-        PyTuple_SET_ITEM(tuple, i++, o);
-    }
-    return tuple;
-}
-
-// A C entry point called without the interpreter lock.  What can throw (a
-// tensor's pointer) is an argument, so it is over before the lock is given up;
-// the entry points themselves let no exception out.
-template <class F, class... A> int without_gil(F entry, A... args)
-{
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = entry(args...);
-    Py_END_ALLOW_THREADS
-    return status;
-}
-
-// The last two arguments of every call: device index and stream handle.
-template <class F> PyObject *plain_call(PyObject *const *args, Py_ssize_t n, Py_ssize_t expected, F &&body)
-{
-    HANDLE_TH_ERRORS
-    if (n != expected) {
-        PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
-        return nullptr;
-    }
-    const Call call{PyLong_AsLongLong(args[n - 2]), PyLong_AsVoidPtr(args[n - 1])};
-    if (PyErr_Occurred())
-        return nullptr;
-    try {
-        return body(call);
-    } catch (const NotPlain &) {
-        Py_RETURN_NONE;
-    }
-    END_HANDLE_TH_ERRORS
-}
-
-at::Tensor bytes(const at::Tensor &like, size_t n)
-{
-    return n ? at::empty({(int64_t)n}, like.options().dtype(at::kByte)) : at::Tensor();
-}
-
-bool truth(PyObject *o)
-{
-    const int v = PyObject_IsTrue(o);
-    if (v < 0)
-        throw python_error();               // what it raised goes on
-    return v;
-}
 
 // x, weight, bias, silu, state, lens, out, state_out
 PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n)
@@ -338,21 +204,7 @@ PyObject *scores(PyObject *, PyObject *const *a, Py_ssize_t n)
 }
 
 // bind(address of each entry point, in the order of Entries)
-PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
-{
-    void *entries[sizeof(Entries) / sizeof(void *)];
-    if (n != (Py_ssize_t)(sizeof(entries) / sizeof(void *))) {
-        PyErr_SetString(PyExc_TypeError, "wrong number of entry points");
-        return nullptr;
-    }
-    for (Py_ssize_t i = 0; i < n; ++i)
-        entries[i] = PyLong_AsVoidPtr(a[i]);
-    if (PyErr_Occurred())
-        return nullptr;
-    static_assert(sizeof(entries) == sizeof(lib), "an address for each");
-    __builtin_memcpy((void *)&lib, entries, sizeof(lib));
-    Py_RETURN_NONE;
-}
+PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) { return bind_entries(lib, a, n); }
 
 template <class F> constexpr PyCFunction method(F f) { return (PyCFunction)(void (*)(void))f; }
 
@@ -363,6 +215,11 @@ PyMethodDef methods[] = {
     {"quantize", method(quantize), METH_FASTCALL, nullptr},
     {"project", method(project), METH_FASTCALL, nullptr},
     {"scores", method(scores), METH_FASTCALL, nullptr},
+    {"bind_delta", method(bind_delta), METH_FASTCALL, nullptr},
+    {"delta", method(delta_call), METH_FASTCALL, nullptr},
+    {"norm", method(norm_call), METH_FASTCALL, nullptr},
+    {"beam", method(beam_call), METH_FASTCALL, nullptr},
+    {"reorder", method(reorder_call), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,

@@ -231,6 +231,42 @@ struct ScoresArgs {
     void *workspace;
 };
 
+struct DeltaArgs {
+    rnn_delta_desc d;
+    const void *q, *k, *v, *beta, *g;
+    const float *A, *dt_bias, *state_in;
+    const int32_t *lens;
+    void *o, *workspace;
+    float *state_out;
+};
+
+struct NormArgs {
+    rnn_norm_desc d;
+    const void *x, *z;
+    const float *weight;
+    void *y;
+};
+
+struct BeamArgs {
+    rnn_beam_desc d;
+    const void *logits;
+    const float *scores;
+    const uint8_t *finished;
+    float *out_scores;
+    int32_t *out_tokens, *out_parents;
+    void *workspace;
+};
+
+// What one launch reorders; first[i] is the first workgroup of item i.
+constexpr int kReorderItems = 32;
+struct ReorderArgs {
+    int64_t batch, beams, keep;
+    const int32_t *parents;
+    int32_t count;
+    uint32_t first[kReorderItems + 1];
+    rnn_reorder_item items[kReorderItems];
+};
+
 // Whether a launch can have so many workgroups: a grid's threads are counted in 32 bits.
 inline bool launchable(uint64_t workgroups, uint32_t threads) { return workgroups <= 0xFFFFFFFFu / threads; }
 
@@ -244,5 +280,12 @@ size_t project_workspace(const rnn_quant_desc &d);
 int launch_project(const ProjectArgs &a, hipStream_t s);
 size_t scores_workspace(const rnn_scores_desc &d);
 int launch_scores(const ScoresArgs &a, hipStream_t s);
+size_t delta_workspace(const rnn_delta_desc &d);
+int launch_delta(const DeltaArgs &a, hipStream_t s);
+int launch_norm(const NormArgs &a, hipStream_t s);
+size_t beam_workspace(const rnn_beam_desc &d);
+int launch_beam(const BeamArgs &a, hipStream_t s);
+int reorder_fits(ReorderArgs &a);      // fills in `first`, enqueues nothing
+int launch_reorder(ReorderArgs &a, hipStream_t s);
 
 }  // namespace rnnamd
