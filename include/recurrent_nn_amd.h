@@ -517,9 +517,10 @@ typedef struct rnn_delta_desc {
  * first step, state_out (nullable) = S after the last one.  One new token is a
  * call with steps = 1.
  *   Longer calls take their steps in chunks of 64, whose corrections solve a
- *   triangular system: the same sums in another order.  A row's result does not
- *   depend on the other rows, but the choice between chunks and single steps is
- *   made for the whole call.
+ *   triangular system: the same sums in another order, so that a key, value or gate
+ *   that is not finite reaches the outputs of its head from its chunk's first step
+ *   on.  A row's result does not depend on the other rows, but the choice between
+ *   chunks and single steps is made for the whole call.
  *   g, A (needs g), dt_bias (needs A), state_in, sequence_lens, state_out may be NULL.
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
  *   key_dim outside 1 to RNN_DELTA_MAX_KEY_DIM, key_heads that do not divide

@@ -40,4 +40,8 @@ __device__ __forceinline__ float key_scale(float squares, int32_t normalize)
     return normalize ? 1.0f / sqrtf(squares + RNN_DELTA_KEY_EPS) : 1.0f;
 }
 
+// Chunks of 64 steps (lm_delta_chunk.hip); sizes are not zero.
+size_t delta_chunks_workspace(const rnn_delta_desc &d);
+int launch_delta_chunks(const DeltaArgs &a, hipStream_t s);
+
 }  // namespace rnnamd

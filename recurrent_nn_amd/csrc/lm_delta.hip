@@ -217,10 +217,14 @@ template <class T> static int delta_go(const DeltaArgs &a, hipStream_t s)
     return a.d.key_dim <= 192 ? steps_go<T, 24>(a, s) : steps_go<T, 32>(a, s);
 }
 
-size_t delta_workspace(const rnn_delta_desc &) { return 0; }
+static bool in_chunks(const rnn_delta_desc &d) { return d.steps > 32; }
+
+size_t delta_workspace(const rnn_delta_desc &d) { return in_chunks(d) ? delta_chunks_workspace(d) : 0; }
 
 int launch_delta(const DeltaArgs &a, hipStream_t s)
 {
+    if (in_chunks(a.d))
+        return launch_delta_chunks(a, s);
     switch (a.d.dtype) {
     case RNN_DTYPE_F32: return delta_go<F32>(a, s);
     case RNN_DTYPE_BF16: return delta_go<BF16>(a, s);

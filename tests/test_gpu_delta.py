@@ -200,7 +200,7 @@ def test_zero_keys_and_rates(steps):
 
 @pytest.mark.parametrize("steps", [1, 100])
 def test_what_is_not_finite_stays_in_its_row_and_column(steps):
-    x = case(Draw(15), 3, steps, 1, 2, 64, 40, F32, "log", True, True, False)
+    x = case(Draw(15), 3, steps, 2, 2, 64, 40, F32, "log", True, True, False)
     o, err, S, S_err = expected(x)
     at = steps // 2
     dev = on_device(x)
@@ -209,13 +209,28 @@ def test_what_is_not_finite_stays_in_its_row_and_column(steps):
     got, end = ra.gated_delta(**dev)
     assert_close(got[0], o[0], err[0], "row 0")
     assert_close(end[0], S[0], S_err[0], "row 0")
-    # one value column of one head; the steps before it are untouched
+    # one value column of one head
     others = [c for c in range(40) if c != 7]
     assert_close(got[1][:, 0][:, others], o[1][:, 0][:, others], err[1][:, 0][:, others], "columns")
     assert_close(got[1][:, 1], o[1][:, 1], err[1][:, 1], "the other head")
     assert not torch.isfinite(got[1, at:, 0, 7]).any()
-    assert_close(got[2][:at], o[2][:at], err[2][:at], "steps before")
-    assert got[2, at:].isnan().all() and end[2].isnan().all()
+    # one head, whose chunk of 64 steps begins at 0: its later steps, not the other's
+    assert got[2, at:, 0].isnan().all() and end[2, 0].isnan().all()
+    assert_close(got[2][:, 1], o[2][:, 1], err[2][:, 1], "the other head")
+
+
+def test_what_is_not_finite_leaves_earlier_chunks():
+    x = case(Draw(22), 1, 200, 2, 2, 64, 40, BF16, "log", True, True, False)
+    o, err, S, S_err = expected(x)
+    dev = on_device(x)
+    dev["q"][0, 130, 1, 5] = dev["k"][0, 140, 0, 3] = NAN
+    got, end = ra.gated_delta(**dev)
+    assert_close(got[:, :128], o[:, :128], err[:, :128], "o")
+    assert got[0, 140:, 0].isnan().all() and got[0, 130, 1].isnan().all()
+    # a query is read by its own step alone
+    others = [t for t in range(200) if t != 130]
+    assert_close(got[:, others][:, :, 1], o[:, others][:, :, 1], err[:, others][:, :, 1], "the other steps")
+    assert_close(end[:, 1], S[:, 1], S_err[:, 1], "state")
 
 
 def test_lengths_beyond_their_range_are_bounded():
