@@ -47,9 +47,13 @@ INST_UNITS = [(fam, act) for fam in range(5) for act in range(5)]
 FAMILY_FLAGS = {1: ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 2: ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
+# The delta rule's products are read by ordinary instructions and are operands
+# of the next ones: accumulation registers would be copied at each.
+FILE_FLAGS = {"lm_delta_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+
 # (source, extra flags, object name) of every translation unit: the .hip
 # files of csrc, the instantiation units, the HIP host code
-HIP_UNITS = ([(f, [], f + ".o") for f in sorted(os.listdir(CSRC))
+HIP_UNITS = ([(f, FILE_FLAGS.get(f, []), f + ".o") for f in sorted(os.listdir(CSRC))
               if f.endswith(".hip") and f != INST] +
              [(INST, [f"-DRNN_FAMILY={fam}", f"-DRNN_ACT={act}", *FAMILY_FLAGS.get(fam, [])],
                f"recurrence_inst_f{fam}_a{act}.o") for fam, act in INST_UNITS] +

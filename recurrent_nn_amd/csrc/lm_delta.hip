@@ -217,7 +217,14 @@ template <class T> static int delta_go(const DeltaArgs &a, hipStream_t s)
     return a.d.key_dim <= 192 ? steps_go<T, 24>(a, s) : steps_go<T, 32>(a, s);
 }
 
-static bool in_chunks(const rnn_delta_desc &d) { return d.steps > 32; }
+// Chunks from so many steps on, where the rows of a chunk lie within what 32 bits of
+// a lane's address reach.
+static bool in_chunks(const rnn_delta_desc &d)
+{
+    const int64_t most = ((int64_t)1 << 31) / (64 * (d.dtype == RNN_DTYPE_F32 ? 4 : 2)) - 65536;
+    return d.steps > 32 && d.q_step_stride < most && d.k_step_stride < most && d.v_step_stride < most &&
+           d.o_step_stride < most && d.value_dim < 65536;
+}
 
 size_t delta_workspace(const rnn_delta_desc &d) { return in_chunks(d) ? delta_chunks_workspace(d) : 0; }
 

@@ -58,25 +58,31 @@ __device__ __forceinline__ v4f mfma(float a, float b, v4f c)
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// Plane p of x, taken off it.
-__device__ __forceinline__ __bf16 next_plane(float &x)
-{
-    const __bf16 p = (__bf16)x;
-    x -= (float)p;
-    return p;
-}
-template <int P> __device__ __forceinline__ void planes_of(const float (&x)[8], v8b (&out)[P])
-{
-    float rest[8];
+// N values (an even number) as planes: P bfloat16 values that add up to each, the
+// first the nearest, each other the nearest to what is left.  Two values a
+// conversion; the last plane's remainder is not taken.
+template <int P, int N> struct Planes {
+    uint32_t pair[P][N / 2];
+    __device__ __forceinline__ explicit Planes(const float (&x)[N])
+    {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        rest[j] = x[j];
+        for (int j = 0; j < N / 2; ++j) {
+            float lo = x[2 * j], hi = x[2 * j + 1];
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            out[p][j] = next_plane(rest[j]);
-}
+            for (int p = 0; p < P; ++p) {
+                typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+                typedef float v2f __attribute__((ext_vector_type(2)));
+                const uint32_t both = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{lo, hi}), v2b));
+                pair[p][j] = both;
+                if (p + 1 < P) {
+                    lo -= __uint_as_float(both << 16);
+                    hi -= __uint_as_float(both & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void put(int p, void *to) const { __builtin_memcpy(to, pair[p], 2 * N); }
+};
 
 // Row m of tile w of a chunk (or of a state), and the place of a row in that order.
 __device__ __forceinline__ int row_of(int w, int m) { return 32 * (w / 2) + 8 * (m / 4) + 4 * (w % 2) + m % 4; }
@@ -120,9 +126,9 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
     constexpr int KP = kPlanes<T>, PP = kOutLast<T> + 1, LDK = 32 * KB + 8, LDT = 68;
     using Sizes = DeltaSizes<T, KB>;
     __shared__ __attribute__((aligned(16))) __bf16 keys[KP][kChunk][LDK];
-    __shared__ __attribute__((aligned(16))) float Lm[kChunk][LDT], Pm[kChunk][LDT], Tm[kChunk][LDT];
-    __shared__ float2 G2[kChunk];
-    __shared__ float rates[kChunk], rk[kChunk], rq[kChunk];
+    __shared__ __attribute__((aligned(16))) float Lt[kChunk][LDT], Tm[kChunk][LDT];    // L transposed; P, then T
+    __shared__ float2 G2[kChunk];               // sums of log2 decays, and what float32 leaves of them
+    __shared__ __attribute__((aligned(16))) float rates[kChunk], rk[kChunk], rq[kChunk];
     const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
     const int n16 = lane % 16, g = lane / 16;
     const Place pl = place_in(sp.count);
@@ -141,39 +147,57 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
 
     // this wave's rows of K and Q, as planes
     const int row = row_of(w, n16);
-    auto load = [&](const void *base, int64_t bs, int64_t ss, int64_t hs, v8b (&out)[KB][KP]) {
-        const raw *at = (const raw *)base + b * bs + key_head * hs +
-                        (int64_t)(start + (row < here ? row : here - 1)) * ss;
-        float squares = 0.0f;
+    const raw *k_at = (const raw *)a.k + b * a.d.k_batch_stride + key_head * a.d.k_head_stride +
+                      (int64_t)(start + (row < here ? row : here - 1)) * a.d.k_step_stride;
+    const raw *q_at = (const raw *)a.q + b * a.d.q_batch_stride + key_head * a.d.q_head_stride +
+                      (int64_t)(start + (row < here ? row : here - 1)) * a.d.q_step_stride;
+    Pack<T, 8> kv[KB], qv[KB];
+    auto load = [&](const raw *at, Pack<T, 8> (&v)[KB]) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int col = 32 * kb + 8 * g;
-            float x[8];
             if (DIRECT || dk == 32 * KB) {
-                const Pack<T, 8> v = load_pack<T, 8>(at + col);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[j] = T::load(v.v[j]);
+                v[kb] = load_pack<T, 8>(at + col);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float v = T::load(at[col + j < dk ? col + j : dk - 1]);
-                    x[j] = col + j < dk ? v : 0.0f;
+                    const raw x = at[col + j < dk ? col + j : dk - 1];
+                    v[kb].v[j] = col + j < dk ? x : (raw)0;
                 }
             }
+        }
+    };
+    load(k_at, kv);
+    load(q_at, qv);
+    float beta = 0.0f, log_g = 0.0f;
+    if (w == 0 && lane < here) {
+        const int64_t t = start + lane;
+        beta = gate_at<T>(a.beta, a.d.gate_dtype, b * a.d.beta_batch_stride + t * a.d.beta_step_stride + head);
+        if (a.g)
+            log_g = gate_at<T>(a.g, a.d.gate_dtype, b * a.d.g_batch_stride + t * a.d.g_step_stride + head);
+    }
+    v8b kf[KB][KP], qf[KB][KP];
+    auto planes = [&](const Pack<T, 8> (&v)[KB], v8b (&out)[KB][KP]) {
+        float squares = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = row < here ? x[j] : 0.0f;
-                squares = __builtin_fmaf(x[j], x[j], squares);
-            }
-            planes_of<KP>(x, out[kb]);
+        for (int kb = 0; kb < KB; ++kb) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = row < here ? T::load(v[kb].v[j]) : 0.0f;
+            if (a.d.normalize)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    squares = __builtin_fmaf(x[j], x[j], squares);
+            const Planes<KP, 8> p(x);
+#pragma unroll
+            for (int s = 0; s < KP; ++s)
+                p.put(s, &out[kb][s]);
         }
         squares += __shfl_xor(squares, 16);
         return squares + __shfl_xor(squares, 32);
     };
-    v8b kf[KB][KP], qf[KB][KP];
-    const float kk = load(a.k, a.d.k_batch_stride, a.d.k_step_stride, a.d.k_head_stride, kf);
-    const float qq = load(a.q, a.d.q_batch_stride, a.d.q_step_stride, a.d.q_head_stride, qf);
+    const float kk = planes(kv, kf), qq = planes(qv, qf);
     if (g == 0) {
         rk[row] = key_scale(kk, a.d.normalize);
         rq[row] = key_scale(qq, a.d.normalize) * a.d.scale;
@@ -194,82 +218,114 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
             }
     }
     if (w == 0) {                               // gates, a step a lane
-        float decay = 0.0f, rate = 0.0f;
-        if (lane < here) {
-            const int64_t t = start + lane;
-            rate = rate_of(gate_at<T>(a.beta, a.d.gate_dtype,
-                                      b * a.d.beta_batch_stride + t * a.d.beta_step_stride + head),
-                           a.d.beta_sigmoid);
-            if (a.g)
-                decay = log_decay(gate_at<T>(a.g, a.d.gate_dtype,
-                                             b * a.d.g_batch_stride + t * a.d.g_step_stride + head),
-                                  a.A != nullptr, a.A ? a.A[head] : 0.0f, a.dt_bias ? a.dt_bias[head] : 0.0f);
-        }
-        double sum = decay;
+        double sum = 0.0;
+        if (a.g && lane < here)
+            sum = log_decay(log_g, a.A != nullptr, a.A ? a.A[head] : 0.0f, a.dt_bias ? a.dt_bias[head] : 0.0f);
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const double before = __shfl_up(sum, d);
             sum += lane >= d ? before : 0.0;
         }
+        sum *= 1.4426950408889634074;
         G2[lane] = {(float)sum, (float)(sum - (double)(float)sum)};
-        rates[lane] = rate;
+        rates[lane] = lane < here ? rate_of(beta, a.d.beta_sigmoid) : 0.0f;
     }
     __syncthreads();
-    auto apart = [&](float2 x, float2 y) { return expf((x.x - y.x) + (x.y - y.y)); };
-    if (tid < kChunk) {
+    auto apart = [&](float2 x, float2 y) { return __builtin_amdgcn_exp2f((x.x - y.x) + (x.y - y.y)); };
+    if (w == 3) {
         float *vec = (float *)(sp.vec + unit * Sizes::vec);
-        const float2 G = G2[tid];
-        const float D = expf(G.x + G.y);
-        vec[place_of(tid)] = D * rk[tid];
-        vec[64 + place_of(tid)] = D * rq[tid];
-        vec[128 + place_of(tid)] = tid < here ? apart(G2[kChunk - 1], G) * rk[tid] : 0.0f;
-        if (tid == kChunk - 1)
+        const float2 G = G2[lane];
+        const float D = __builtin_amdgcn_exp2f(G.x + G.y);
+        vec[place_of(lane)] = D * rk[lane];
+        vec[64 + place_of(lane)] = D * rq[lane];
+        vec[128 + place_of(lane)] = lane < here ? apart(G2[kChunk - 1], G) * rk[lane] : 0.0f;
+        if (lane == kChunk - 1)
             vec[192] = D;
-        *(v4f *)(vec + kZeros + 4 * tid) = v4f{};
+        *(v4f *)(vec + kZeros + 4 * lane) = v4f{};
     }
 
-    // L and P, the lower triangle in tiles of 16 columns
-    for (int c = 0; c < (w < 2 ? 2 : 4); ++c) {
-        v4f kc = {}, qc = {};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int p = 0; p < KP; ++p) {
-                const v8b other = *(const v8b *)&keys[p][16 * c + n16][32 * kb + 8 * g];
-#pragma unroll
-                for (int s = 0; s < KP; ++s)
-                    if (s + p <= 2) {
-                        kc = mfma(kf[kb][s], other, kc);
-                        qc = mfma(qf[kb][s], other, qc);
-                    }
-            }
-        const int j = 16 * c + n16;
-        const float2 Gj = G2[j];
-        const float rj = rk[j];
+    // L and P, the lower triangle in tiles of 16 columns.  A lane has four of L's rows
+    // of a column, and (its operands in the other order) four of P's columns of a row.
+    {
+        const int i0 = row_of(w, 4 * g);
+        float2 Gi[4];
+        float fi[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = row_of(w, 4 * g + r);
-            const float e = apart(G2[i], Gj) * rj;
-            Lm[i][j] = j < i ? rates[i] * rk[i] * e * kc[r] : 0.0f;
-            Pm[i][j] = j <= i ? rq[i] * e * qc[r] : 0.0f;
+            Gi[r] = G2[i0 + r];
+            fi[r] = rates[i0 + r] * rk[i0 + r];
+        }
+        const float2 Gq = G2[row];
+        const float rqi = rq[row];
+        for (int c = 0; c < (w < 2 ? 2 : 4); ++c) {
+            v4f kc = {}, qc = {};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int p = 0; p < KP; ++p) {
+                    const v8b other = *(const v8b *)&keys[p][16 * c + n16][32 * kb + 8 * g];
+#pragma unroll
+                    for (int s = 0; s < KP; ++s)
+                        if (s + p <= 2) {
+                            kc = mfma(kf[kb][s], other, kc);
+                            qc = mfma(other, qf[kb][s], qc);
+                        }
+                }
+            const int j = 16 * c + n16, j0 = 16 * c + 4 * g;
+            const float2 Gj = G2[j];
+            const float rj = rk[j];
+            v4f l, p;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                l[r] = j < i0 + r ? fi[r] * (apart(Gi[r], Gj) * rj) * kc[r] : 0.0f;
+                p[r] = j0 + r <= row ? rqi * (apart(Gq, G2[j0 + r]) * rk[j0 + r]) * qc[r] : 0.0f;
+            }
+            *(v4f *)&Lt[j][i0] = l;
+            *(v4f *)&Tm[row][j0] = p;
         }
     }
     __syncthreads();
-    // (1 + L)^-1: the blocks on the diagonal, a column a lane
+    // operands of the lower triangles, eight columns of a row a lane
+    auto operands = [&](int item, auto &&values, char *to, auto planes_of) {
+        constexpr int P = decltype(planes_of)::value;
+        const int f = item / 64, l = item % 64;
+        const int tile = f < 2 ? f : (f + 2) / 2, p = f < 2 ? 0 : f % 2;
+        float x[8];
+        values(row_of(tile, l % 16), 32 * p + 8 * (l / 16), x);
+        const Planes<P, 8> out(x);
+        to += (size_t)f * P * kFragment + l * 16;
+#pragma unroll
+        for (int s = 0; s < P; ++s)
+            out.put(s, to + s * kFragment);
+    };
+    for (int item = tid; item < kLower * 64; item += 256)
+        operands(item, [&](int i, int j, float (&x)[8]) {
+            __builtin_memcpy(x, &Tm[i][j], 32);
+        }, sp.p + unit * Sizes::p, std::integral_constant<int, PP>{});
+    // (1 + L)^-1: the blocks on the diagonal, a column a lane, each entry taken off all
+    // below it
+    float t[16];
     {
         const int at = 16 * w;
-        float t[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            t[i] = i == n16 ? 1.0f : 0.0f;
-#pragma unroll
-            for (int k = 0; k < i; ++k)
-                t[i] = __builtin_fmaf(-Lm[at + i][at + k], t[k], t[i]);
-        }
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (i / 4 == g)
-                Tm[at + i][at + n16] = t[i];
+            t[i] = i == n16 ? 1.0f : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 15; ++k) {
+            float l[16];
+#pragma unroll
+            for (int i = (k + 1) / 4 * 4; i < 16; i += 4)
+                __builtin_memcpy(&l[i], &Lt[at + k][at + i], 16);
+#pragma unroll
+            for (int i = k + 1; i < 16; ++i)
+                t[i] = __builtin_fmaf(-l[i], t[k], t[i]);
+        }
+    }
+    __syncthreads();                            // (P has been read)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float v = g == 0 ? t[r] : g == 1 ? t[4 + r] : g == 2 ? t[8 + r] : t[12 + r];
+        Tm[16 * w + 4 * g + r][16 * w + n16] = v;
     }
     // and those below: T_ij = -T_ii sum_k L_ik T_kj
 #pragma unroll
@@ -282,40 +338,27 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
             for (int k = 0; k < far; ++k)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    x = mfma(Lm[i + n16][j + 16 * k + 4 * g + s], Tm[j + 16 * k + 4 * g + s][j + n16], x);
+                    x = mfma(Lt[j + 16 * k + 4 * g + s][i + n16], Tm[j + 16 * k + 4 * g + s][j + n16], x);
+            float own[4];
+            __builtin_memcpy(own, &Tm[i + n16][i + 4 * g], 16);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                y = mfma(Tm[i + n16][i + 4 * g + s], x[s], y);
+                y = mfma(own[s], x[s], y);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 Tm[i + 4 * g + r][j + n16] = -y[r];
         }
     }
     __syncthreads();
-    // operands of the lower triangles, eight columns of a row a lane
-    for (int item = tid; item < kLower * 64; item += 256) {
-        const int f = item / 64, l = item % 64;
-        const int tile = f < 2 ? f : (f + 2) / 2, p = f < 2 ? 0 : f % 2;
-        const int i = row_of(tile, l % 16), j = 32 * p + 8 * (l / 16);
-        float x[8];
-        v8b tp[3], pp[PP];
+    for (int item = tid; item < kLower * 64; item += 256)
+        operands(item, [&](int i, int j, float (&x)[8]) {
+            float rate[8];
+            __builtin_memcpy(x, &Tm[i][j], 32);
+            __builtin_memcpy(rate, &rates[j], 32);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = j + e <= i ? Tm[i][j + e] * rates[j + e] : 0.0f;
-        planes_of<3>(x, tp);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            x[e] = Pm[i][j + e];
-        planes_of<PP>(x, pp);
-        char *to = sp.t + unit * Sizes::t + (size_t)f * 3 * kFragment + l * 16;
-#pragma unroll
-        for (int s = 0; s < 3; ++s)
-            *(v8b *)(to + s * kFragment) = tp[s];
-        to = sp.p + unit * Sizes::p + (size_t)f * PP * kFragment + l * 16;
-#pragma unroll
-        for (int s = 0; s < PP; ++s)
-            *(v8b *)(to + s * kFragment) = pp[s];
-    }
+            for (int e = 0; e < 8; ++e)
+                x[e] = j + e <= i ? x[e] * rate[e] : 0.0f;
+        }, sp.t + unit * Sizes::t, std::integral_constant<int, 3>{});
     // K transposed: eight steps of a row of the state a lane
     if (head % each == 0)
         for (int item = tid; item < 4 * KB * 64; item += 256) {
@@ -341,14 +384,53 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// What a wave reads of a chunk.  The first four waves, a tile of its rows each, carry
+// the state along; four others, beside them, make the outputs.
+template <class T, int KB> struct StateOperands {
+    static constexpr int KP = kPlanes<T>, TW = (2 * KB + 3) / 4;
+    v8b k[KB][KP], t[2][3], kt[TW][2][KP];
+    typename T::raw v[4];
+    v4f k_row, w_row;
+    float D;
+    static constexpr int registers = 4 * (KB * KP + 6 + 2 * TW * KP) + 13;
+};
+template <class T, int KB> struct OutOperands {
+    static constexpr int KP = kPlanes<T>, PP = kOutLast<T> + 1;
+    v8b q[KB][KP], p[2][PP];
+    v4f q_row;
+    static constexpr int registers = 4 * (KB * KP + 2 * PP) + 4;
+};
+// Two chunks are on their way where the registers of a wave (256) hold them.
+template <class Operands> constexpr int kAhead = Operands::registers <= 90 ? 2 : 1;
+
+// f(operands of the chunk, chunk, the chunk whose operands take their place) for each
+// chunk of [first, last).
+template <int AHEAD, class Operands, class Load, class F>
+__device__ __forceinline__ void along(int first, int last, Load &&load, F &&f)
+{
+    Operands x[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        load(x[i], first + i < last ? first + i : last - 1);
+    lds_barrier();                              // (the state is published)
+    auto next = [&](int c) { return c + AHEAD < last ? c + AHEAD : last - 1; };
+    int c = first;
+    for (; c + AHEAD <= last; c += AHEAD)       // (no way round a load: waits are by their number)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            f(x[i], c + i, next(c + i));
+    if (c < last)
+        f(x[0], c, last - 1);
+}
+
 template <class T, int KB, bool DIRECT>
-__global__ __launch_bounds__(256) void delta_chunks_kernel(DeltaArgs a, DeltaSpan sp, uint32_t slices)
+__global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpan sp, uint32_t slices)
 {
     using raw = typename T::raw;
     using Sizes = DeltaSizes<T, KB>;
     constexpr int KP = kPlanes<T>, LAST = kOutLast<T>, PP = LAST + 1, TILES = 2 * KB, TW = (TILES + 3) / 4;
     __shared__ v8b Sf[KB][3][64], Rf[2][3][64], Uf[2][PP][64], Wf[2][3][64];
-    const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
+    const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), w = wave % 4;
     const int n16 = lane % 16, g = lane / 16;
     const Place pl = place_in(slices);
     const uint32_t heads = (uint32_t)a.d.heads;
@@ -357,253 +439,257 @@ __global__ __launch_bounds__(256) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
         return;
     const int n = delta_steps(a, b), steps = (int)a.d.steps;
     const int dk = (int)a.d.key_dim, dv = (int)a.d.value_dim, col = (int)pl.at * 16 + n16;
-    const bool in = col < dv;
+    const bool in = col < dv, all_in = (int)pl.at * 16 + 16 <= dv;
     const int64_t key_head = head / (a.d.heads / a.d.key_heads);
     const int first = (int)sp.first, all = (n + kChunk - 1) / kChunk;
     const int last = first + (int)sp.count < all ? first + (int)sp.count : all;     // chunks [first, last)
 
-    // the state: this wave's tiles in registers, everyone's as operands in LDS
-    v4f S[TW];
-    const int64_t state_at = (int64_t)pl.bh * dk * dv + col;
-    auto publish = [&]() {
-#pragma unroll
-        for (int x = 0; x < TW; ++x) {
-            const int tile = w * TW + x;
-            if (tile < TILES) {
-                v4f rest = S[x];
-#pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    v4b out;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        out[r] = next_plane(((float *)&rest)[r]);
-                    ((v4b *)&Sf[tile / 2][p][lane])[tile % 2] = out;
-                }
-            }
-        }
-    };
-#pragma unroll
-    for (int x = 0; x < TW; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = row_of(w * TW + x, 4 * g + r);
-            S[x][r] = sp.from && in && row < dk ? sp.from[state_at + (int64_t)row * dv] : 0.0f;
-        }
-
+    // Addresses: a base for all lanes that moves along, and 32 bits of a lane (the rows of
+    // 64 steps span less than 2^31 bytes).
     const int row = row_of(w, n16), out_row = row_of(w, 4 * g);
-    const raw *k_at = (const raw *)a.k + b * a.d.k_batch_stride + key_head * a.d.k_head_stride;
-    const raw *q_at = (const raw *)a.q + b * a.d.q_batch_stride + key_head * a.d.q_head_stride;
-    const raw *v_at = (const raw *)a.v + b * a.d.v_batch_stride + head * a.d.v_head_stride + (in ? col : dv - 1);
-    raw *o_at = (raw *)a.o + b * a.d.o_batch_stride + head * a.d.o_head_stride + col;
+    char *o_at = (char *)a.o + (b * a.d.o_batch_stride + head * a.d.o_head_stride) * sizeof(raw);
+    const uint32_t o_step = (uint32_t)a.d.o_step_stride * sizeof(raw);
+    const uint32_t v_col = (uint32_t)(in ? col : dv - 1) * sizeof(raw);
     const size_t unit0 = (size_t)pl.bh * sp.count;
     const size_t key_unit0 = (size_t)(b * a.d.key_heads + key_head) * sp.count;
-
-    v8b kf[KB][KP], qf[KB][KP], tf[2][3], pf[2][PP], ktf[TW][2][KP];
-    raw v[4];
-    v4f dk_row, dq_row, w_row;
-    float D;
-    auto load_rows = [&](int c) {
+    const uint32_t lane16 = lane * 16, row_at = (16 * w + 4 * g) * sizeof(float);
+    auto operand = [&](const char *base) { return *(const v8b *)(base + lane16); };
+    auto vec_of = [&](int c) { return sp.vec + (unit0 + c - first) * Sizes::vec; };
+    // This wave's rows of K (0) or Q (1).
+    auto load_rows = [&](const void *base, int64_t bs, int64_t ss, int64_t hs, int which, int c, v8b (&x)[KB][KP]) {
         if (DIRECT) {
-            const int t = kChunk * c + row;
-            const int64_t at = t < n ? t : n - 1;
+            const int most = n - 1 - kChunk * c;        // the last row of the chunk that is there
+            const uint32_t step = (uint32_t)ss * sizeof(raw), at = (row < most ? row : most) * step + 16 * g;
+            const char *from = (const char *)base + (b * bs + key_head * hs) * sizeof(raw) + (size_t)c * kChunk * step;
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                kf[kb][0] = __builtin_bit_cast(v8b, load_pack<T, 16 / sizeof(raw)>(
-                                                        k_at + at * a.d.k_step_stride + 32 * kb + 8 * g));
-                qf[kb][0] = __builtin_bit_cast(v8b, load_pack<T, 16 / sizeof(raw)>(
-                                                        q_at + at * a.d.q_step_stride + 32 * kb + 8 * g));
-            }
+            for (int kb = 0; kb < KB; ++kb)
+                x[kb][0] = __builtin_bit_cast(v8b, load_pack<BF16, 8>((const uint16_t *)(from + at) + 32 * kb));
         } else {
-            const char *at = sp.packed + (key_unit0 + c - first) * (2 * Sizes::kt) +
-                             (size_t)w * KB * KP * kFragment + lane * 16;
+            const char *at = sp.packed + (key_unit0 + c - first) * (2 * Sizes::kt) + which * Sizes::kt +
+                             (size_t)w * KB * KP * kFragment;
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int p = 0; p < KP; ++p) {
-                    kf[kb][p] = *(const v8b *)(at + (kb * KP + p) * kFragment);
-                    qf[kb][p] = *(const v8b *)(at + Sizes::kt + (kb * KP + p) * kFragment);
-                }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = kChunk * c + out_row + r;
-            v[r] = v_at[(int64_t)(t < n ? t : n - 1) * a.d.v_step_stride];
+                for (int p = 0; p < KP; ++p)
+                    x[kb][p] = operand(at + (kb * KP + p) * kFragment);
         }
     };
-    auto load_vec = [&](int c) {
-        const float *vec = (const float *)(sp.vec + (unit0 + c - first) * Sizes::vec);
-        dk_row = *(const v4f *)(vec + 16 * w + 4 * g);
-        dq_row = *(const v4f *)(vec + 64 + 16 * w + 4 * g);
-        w_row = *(const v4f *)(vec + 128 + 16 * w + 4 * g);
-        D = vec[192];
-    };
-    // Tiles 0 and 1 have nothing beyond the diagonal: zeros in the place of a second
-    // operand, since a branch around its products loses the wait that reading the
-    // others' results needs.
-    auto lower = [&](const char *at, const char *zeros, int p, int s, int planes) {
-        return *(const v8b *)(p == 1 && w < 2 ? zeros : at + (size_t)(lower_of(w, p) * planes + s) * kFragment);
-    };
-    auto zeros_of = [&](int c) {
-        return sp.vec + (unit0 + c - first) * Sizes::vec + kZeros * sizeof(float) + lane * 16;
-    };
-    auto load_t = [&](int c) {
-        const char *at = sp.t + (unit0 + c - first) * Sizes::t + lane * 16;
+    // Operands of a lower triangle.  Tiles 0 and 1 have nothing beyond the diagonal: zeros
+    // in the place of a second one, since a branch around its products loses the wait that
+    // reading the others' results needs.
+    auto load_lower = [&](const char *at, int c, auto &x) {
+        constexpr int P = sizeof(x[0]) / sizeof(v8b);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int s = 0; s < 3; ++s)
-                tf[p][s] = lower(at, zeros_of(c), p, s, 3);
+            for (int s = 0; s < P; ++s)
+                x[p][s] = operand(p == 1 && w < 2 ? vec_of(c) + kZeros * sizeof(float)
+                                                  : at + (size_t)(lower_of(w, p) * P + s) * kFragment);
     };
-    auto load_pk = [&](int c) {
-        const char *at = sp.p + (unit0 + c - first) * Sizes::p + lane * 16;
+
+    if (wave < 4) {
+        // the state: this wave's tiles in registers, everyone's as operands in LDS
+        using Operands = StateOperands<T, KB>;
+        const char *v_at = (const char *)a.v + (b * a.d.v_batch_stride + head * a.d.v_head_stride) * sizeof(raw);
+        const uint32_t v_step = (uint32_t)a.d.v_step_stride * sizeof(raw);
+        v4f S[TW];
+        const int64_t state_at = (int64_t)pl.bh * dk * dv + col;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int x = 0; x < TW; ++x)
 #pragma unroll
-            for (int s = 0; s < PP; ++s)
-                pf[p][s] = lower(at, zeros_of(c), p, s, PP);
-        at = sp.kt + (key_unit0 + c - first) * Sizes::kt + lane * 16;
-#pragma unroll
-        for (int x = 0; x < TW; ++x) {
-            const int tile = w * TW + x < TILES ? w * TW + x : TILES - 1;
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int s = 0; s < KP; ++s)
-                    ktf[x][p][s] = *(const v8b *)(at + (size_t)((tile * 2 + p) * KP + s) * kFragment);
-        }
-    };
-    if (first < last) {
-        load_rows(first);
-        load_vec(first);
-        load_t(first);
-        load_pk(first);
-        publish();
-        lds_barrier();
-    }
-    for (int c = first; c < last; ++c) {
-        const int next = c + 1 < last ? c + 1 : c, start = kChunk * c;
-        // K S and Q S, and what the corrections solve for
-        v4f x[3] = {}, y[PP] = {};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                const v8b s = Sf[kb][p][lane];
-#pragma unroll
-                for (int e = 0; e < KP; ++e) {
-                    if (e + p <= 2)
-                        x[p] = mfma(kf[kb][e], s, x[p]);
-                    if (e + p <= LAST)
-                        y[p] = mfma(qf[kb][e], s, y[p]);
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int at = row_of(w * TW + x, 4 * g + r);
+                S[x][r] = sp.from && in && at < dk ? sp.from[state_at + (int64_t)at * dv] : 0.0f;
             }
-        float R[4], vr[4];
+        auto publish = [&]() {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            vr[r] = T::load(v[r]);
-        const v4f Y = PP == 3 ? (y[PP - 1] + y[1]) + y[0] : y[1] + y[0];
-        const v4f X = (x[2] + x[1]) + x[0];
+            for (int x = 0; x < TW; ++x) {
+                const int tile = w * TW + x;
+                const float s[4] = {S[x][0], S[x][1], S[x][2], S[x][3]};
+                const Planes<3, 4> out(s);
+                if (4 * TW == TILES || tile < TILES)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            R[r] = start + out_row + r < n ? vr[r] - dk_row[r] * X[r] : 0.0f;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            v4b out;
+                    for (int p = 0; p < 3; ++p)
+                        out.put(p, (v4b *)&Sf[tile / 2][p][lane] + tile % 2);
+            }
+        };
+        auto load_kv = [&](Operands &x, int c) {
+            load_rows(a.k, a.d.k_batch_stride, a.d.k_step_stride, a.d.k_head_stride, 0, c, x.k);
+            const int most = n - 1 - kChunk * c;
+            const char *at = v_at + (size_t)c * kChunk * v_step;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                out[r] = next_plane(R[r]);
-            ((v4b *)&Rf[w / 2][p][lane])[w % 2] = out;
-        }
-        load_rows(next);
-        lds_barrier();
-        // the corrections
-        v4f u[3] = {};
+                x.v[r] = *(const raw *)(at + ((uint32_t)(out_row + r < most ? out_row + r : most) * v_step + v_col));
+            x.k_row = *(const v4f *)(vec_of(c) + row_at);
+        };
+        auto load_t = [&](Operands &x, int c) {
+            load_lower(sp.t + (unit0 + c - first) * Sizes::t, c, x.t);
+            x.w_row = *(const v4f *)(vec_of(c) + 512 + row_at);
+        };
+        auto load_kt = [&](Operands &x, int c) {
+            const char *at = sp.kt + (key_unit0 + c - first) * Sizes::kt;
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+            for (int y = 0; y < TW; ++y) {
+                const int tile = w * TW + y < TILES ? w * TW + y : TILES - 1;
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                const v8b r = Rf[p][s][lane];
+                for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int e = 0; e + s <= 2; ++e)
-                    u[e + s] = mfma(tf[p][e], r, u[e + s]);
+                    for (int s = 0; s < KP; ++s)
+                        x.kt[y][p][s] = operand(at + (size_t)((tile * 2 + p) * KP + s) * kFragment);
             }
-        const v4f U = (u[2] + u[1]) + u[0];
-        load_t(next);
-        {
-            v4f rest = U, scaled;
+            x.D = *(const float *)(vec_of(c) + 768);
+        };
+        if (first < last) {
+            publish();
+            along<kAhead<Operands>, Operands>(first, last, [&](Operands &x, int c) {
+                load_kv(x, c);
+                load_t(x, c);
+                load_kt(x, c);
+            }, [&](Operands &x, int c, int next) {
+                // K S, and what the corrections solve for
+                v4f X[2] = {};
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                scaled[r] = U[r] * w_row[r];
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                v4b out;
-                if (p < PP) {
+                    for (int p = 0; p < 3; ++p) {
+                        const v8b s = Sf[kb][p][lane];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        out[r] = next_plane(((float *)&rest)[r]);
-                    ((v4b *)&Uf[w / 2][p < PP ? p : 0][lane])[w % 2] = out;
-                }
+                        for (int e = 0; e + p <= 2 && e < KP; ++e)
+                            X[e + p > 0] = mfma(x.k[kb][e], s, X[e + p > 0]);
+                    }
+                float R[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    out[r] = next_plane(((float *)&scaled)[r]);
-                ((v4b *)&Wf[w / 2][p][lane])[w % 2] = out;
-            }
-        }
-        lds_barrier();
-        // the outputs and the state
-        v4f o[PP] = {}, d[TW][3] = {};
+                    R[r] = kChunk * c + out_row + r < n ? T::load(x.v[r]) - x.k_row[r] * (X[1][r] + X[0][r]) : 0.0f;
+                const Planes<3, 4> r_out(R);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+                for (int p = 0; p < 3; ++p)
+                    r_out.put(p, (v4b *)&Rf[w / 2][p][lane] + w % 2);
+                load_kv(x, next);
+                lds_barrier();
+                // the corrections
+                v4f u[2] = {};
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                const v8b f = Wf[p][s][lane];
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int s = 0; s < 3; ++s) {
+                        const v8b r = Rf[p][s][lane];
+#pragma unroll
+                        for (int e = 0; e + s <= 2; ++e)
+                            u[e + s > 0] = mfma(x.t[p][e], r, u[e + s > 0]);
+                    }
+                float U[4], W[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    U[r] = u[1][r] + u[0][r];
+                    W[r] = U[r] * x.w_row[r];
+                }
+                const Planes<3, 4> w_out(W);
+                const Planes<PP, 4> u_out(U);
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    w_out.put(p, (v4b *)&Wf[w / 2][p][lane] + w % 2);
+#pragma unroll
+                for (int p = 0; p < PP; ++p)
+                    u_out.put(p, (v4b *)&Uf[w / 2][p][lane] + w % 2);
+                load_t(x, next);
+                lds_barrier();
+                // the state
+                v4f d[TW][2] = {};
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int s = 0; s < 3; ++s) {
+                        const v8b f = Wf[p][s][lane];
+#pragma unroll
+                        for (int t = 0; t < TW; ++t)
+#pragma unroll
+                            for (int e = 0; e + s <= 2 && e < KP; ++e)
+                                d[t][e + s > 0] = mfma(x.kt[t][p][e], f, d[t][e + s > 0]);
+                    }
 #pragma unroll
                 for (int t = 0; t < TW; ++t)
 #pragma unroll
-                    for (int e = 0; e < KP; ++e)
-                        if (e + s <= 2)
-                            d[t][s] = mfma(ktf[t][p][e], f, d[t][s]);
-            }
-#pragma unroll
-            for (int s = 0; s < PP; ++s) {
-                const v8b f = Uf[p][s][lane];
-#pragma unroll
-                for (int e = 0; e + s <= LAST; ++e)
-                    o[e + s] = mfma(pf[p][e], f, o[e + s]);
-            }
+                    for (int r = 0; r < 4; ++r)
+                        S[t][r] = __builtin_fmaf(x.D, S[t][r], d[t][1][r] + d[t][0][r]);
+                publish();
+                load_kt(x, next);
+                lds_barrier();
+            });
         }
 #pragma unroll
-        for (int t = 0; t < TW; ++t)
+        for (int x = 0; x < TW; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = row_of(w * TW + x, 4 * g + r);
+                if (sp.to && in && at < dk)
+                    sp.to[state_at + (int64_t)at * dv] = S[x][r];
+            }
+        return;
+    }
+
+    // the outputs
+    using Operands = OutOperands<T, KB>;
+    auto load_q = [&](Operands &x, int c) {
+        load_rows(a.q, a.d.q_batch_stride, a.d.q_step_stride, a.d.q_head_stride, 1, c, x.q);
+    };
+    auto load_p = [&](Operands &x, int c) {
+        load_lower(sp.p + (unit0 + c - first) * Sizes::p, c, x.p);
+        x.q_row = *(const v4f *)(vec_of(c) + 256 + row_at);
+    };
+    if (first < last)
+        along<kAhead<Operands>, Operands>(first, last, [&](Operands &x, int c) {
+            load_q(x, c);
+            load_p(x, c);
+        }, [&](Operands &x, int c, int next) {
+            lds_barrier();
+            v4f Y[2] = {}, O[2] = {};           // Q S, while the corrections are made
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int p = 0; p <= LAST; ++p) {
+                    const v8b s = Sf[kb][p][lane];
+#pragma unroll
+                    for (int e = 0; e + p <= LAST && e < KP; ++e)
+                        Y[e + p > 0] = mfma(x.q[kb][e], s, Y[e + p > 0]);
+                }
+            load_q(x, next);
+            lds_barrier();
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int s = 0; s < PP; ++s) {
+                    const v8b f = Uf[p][s][lane];
+#pragma unroll
+                    for (int e = 0; e + s <= LAST; ++e)
+                        O[e + s > 0] = mfma(x.p[p][e], f, O[e + s > 0]);
+                }
+            char *to = o_at + (size_t)c * kChunk * o_step;
+            const int start = kChunk * c;
+            raw out[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                S[t][r] = __builtin_fmaf(D, S[t][r], (d[t][2][r] + d[t][1][r]) + d[t][0][r]);
-        publish();
-        const v4f O = PP == 3 ? (o[PP - 1] + o[1]) + o[0] : o[1] + o[0];
+                out[r] = T::store(__builtin_fmaf(x.q_row[r], Y[1][r] + Y[0][r], O[1][r] + O[0][r]));
+            if (all_in && start + kChunk <= n) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = start + out_row + r;
-            if (in && t < n)
-                o_at[t * a.d.o_step_stride] = T::store(__builtin_fmaf(dq_row[r], Y[r], O[r]));
-        }
-        load_pk(next);
-        load_vec(next);
-        lds_barrier();
-    }
+                for (int r = 0; r < 4; ++r)
+                    *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (in && start + out_row + r < n)
+                        *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+            }
+            load_p(x, next);
+            lds_barrier();
+        });
     // steps behind the last one of this span: zeros
     const int from = n > kChunk * first ? n : kChunk * first;
     const int64_t to = (int64_t)kChunk * (first + (int64_t)sp.count);
     const int until = to < steps ? (int)to : steps;
     if (in)
-        for (int t = from + tid / 16; t < until; t += 16)
-            o_at[t * a.d.o_step_stride] = 0;
-#pragma unroll
-    for (int x = 0; x < TW; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int at = row_of(w * TW + x, 4 * g + r);
-            if (sp.to && in && at < dk)
-                sp.to[state_at + (int64_t)at * dv] = S[x][r];
-        }
+        for (int t = from + (tid - 256) / 16; t < until; t += 16)
+            *(raw *)(o_at + (size_t)t * o_step + v_col) = 0;
 }
 
 // The workspace of a span of `count` chunks, as its parts lie in it; then the
@@ -642,7 +728,7 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
     const DeltaLayout l = layout_of<T, KB>(a.d, span, DIRECT);
     const uint64_t rounds = ((uint64_t)a.d.batch * a.d.heads + 7) / 8;
     const uint64_t slices = ((uint64_t)a.d.value_dim + 15) / 16;
-    if (!launchable(rounds * 8 * span, 256) || !launchable(rounds * 8 * slices, 256))
+    if (!launchable(rounds * 8 * span, 256) || !launchable(rounds * 8 * slices, 512))
         return (int)hipErrorInvalidConfiguration;
     char *ws = (char *)a.workspace;
     float *between = a.state_out ? a.state_out : span < all ? (float *)(ws + l.states) : nullptr;
@@ -656,7 +742,7 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
         if (rc)
             return rc;
         delta_chunks_kernel<T, KB, DIRECT>
-            <<<dim3((uint32_t)(rounds * 8 * slices)), dim3(256), 0, s>>>(a, sp, (uint32_t)slices);
+            <<<dim3((uint32_t)(rounds * 8 * slices)), dim3(512), 0, s>>>(a, sp, (uint32_t)slices);
         rc = (int)hipGetLastError();
         if (rc)
             return rc;
