@@ -384,6 +384,28 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Orders what stands before it in a phase: reads of LDS, then the products, with the
+// loads of coming operands between them.  (A load takes the compute unit about 16
+// cycles, and a wave that issues several at once waits for them.)
+template <int READS, int PRODUCTS, int LOADS, int I = -1> __device__ __forceinline__ void spread()
+{
+    constexpr int FIRST = READS < 6 ? READS : 6;
+    if constexpr (I < 0) {
+        __builtin_amdgcn_sched_group_barrier(0x100, FIRST, 0);
+    } else {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        if constexpr (I < READS - FIRST)
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        constexpr int LOAD = (I + 1) * LOADS / PRODUCTS - I * LOADS / PRODUCTS;
+        if constexpr (LOAD > 0)
+            __builtin_amdgcn_sched_group_barrier(0x20, LOAD, 0);
+    }
+    if constexpr (I + 1 < PRODUCTS)
+        spread<READS, PRODUCTS, LOADS, I + 1>();
+}
+// Products of one operand of KP planes with one of three.
+constexpr int kProducts[4] = {0, 3, 5, 6};
+
 // What a wave reads of a chunk.  The first four waves, a tile of its rows each, carry
 // the state along; four others, beside them, make the outputs.
 template <class T, int KB> struct StateOperands {
@@ -403,8 +425,8 @@ template <class T, int KB> struct OutOperands {
 // Two chunks are on their way where the registers of a wave (256) hold them.
 template <class Operands> constexpr int kAhead = Operands::registers <= 90 ? 2 : 1;
 
-// f(operands of the chunk, chunk, the chunk whose operands take their place) for each
-// chunk of [first, last).
+// f(operands of the chunk, of the one before it, chunk, the chunk whose operands take
+// its own's place) for each chunk of [first, last).
 template <int AHEAD, class Operands, class Load, class F>
 __device__ __forceinline__ void along(int first, int last, Load &&load, F &&f)
 {
@@ -418,9 +440,9 @@ __device__ __forceinline__ void along(int first, int last, Load &&load, F &&f)
     for (; c + AHEAD <= last; c += AHEAD)       // (no way round a load: waits are by their number)
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
-            f(x[i], c + i, next(c + i));
+            f(x[i], x[(i + AHEAD - 1) % AHEAD], c + i, next(c + i));
     if (c < last)
-        f(x[0], c, last - 1);
+        f(x[0], x[AHEAD - 1], c, last - 1);
 }
 
 template <class T, int KB, bool DIRECT>
@@ -539,14 +561,17 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
             }
             x.D = *(const float *)(vec_of(c) + 768);
         };
+        __builtin_amdgcn_s_setprio(3);
         if (first < last) {
             publish();
-            along<kAhead<Operands>, Operands>(first, last, [&](Operands &x, int c) {
+            constexpr int AHEAD = kAhead<Operands>;
+            along<AHEAD, Operands>(first, last, [&](Operands &x, int c) {
                 load_kv(x, c);
                 load_t(x, c);
                 load_kt(x, c);
-            }, [&](Operands &x, int c, int next) {
+            }, [&](Operands &x, Operands &before, int c, int next) {
                 // K S, and what the corrections solve for
+                load_kt(before, c + AHEAD - 1 < last ? c + AHEAD - 1 : last - 1);
                 v4f X[2] = {};
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
@@ -557,6 +582,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                         for (int e = 0; e + p <= 2 && e < KP; ++e)
                             X[e + p > 0] = mfma(x.k[kb][e], s, X[e + p > 0]);
                     }
+                spread<3 * KB, KB * kProducts[KP], 2 * TW * KP + 1>();
                 float R[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -565,7 +591,6 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
                     r_out.put(p, (v4b *)&Rf[w / 2][p][lane] + w % 2);
-                load_kv(x, next);
                 lds_barrier();
                 // the corrections
                 v4f u[2] = {};
@@ -578,6 +603,8 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                         for (int e = 0; e + s <= 2; ++e)
                             u[e + s > 0] = mfma(x.t[p][e], r, u[e + s > 0]);
                     }
+                load_kv(x, next);
+                spread<6, 12, KB * KP + 5>();
                 float U[4], W[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -592,7 +619,6 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
 #pragma unroll
                 for (int p = 0; p < PP; ++p)
                     u_out.put(p, (v4b *)&Uf[w / 2][p][lane] + w % 2);
-                load_t(x, next);
                 lds_barrier();
                 // the state
                 v4f d[TW][2] = {};
@@ -607,13 +633,14 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                             for (int e = 0; e + s <= 2 && e < KP; ++e)
                                 d[t][e + s > 0] = mfma(x.kt[t][p][e], f, d[t][e + s > 0]);
                     }
+                load_t(x, next);
+                spread<6, 2 * TW * kProducts[KP], 7>();
 #pragma unroll
                 for (int t = 0; t < TW; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         S[t][r] = __builtin_fmaf(x.D, S[t][r], d[t][1][r] + d[t][0][r]);
                 publish();
-                load_kt(x, next);
                 lds_barrier();
             });
         }
@@ -641,7 +668,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
         along<kAhead<Operands>, Operands>(first, last, [&](Operands &x, int c) {
             load_q(x, c);
             load_p(x, c);
-        }, [&](Operands &x, int c, int next) {
+        }, [&](Operands &x, Operands &, int c, int next) {
             lds_barrier();
             v4f Y[2] = {}, O[2] = {};           // Q S, while the corrections are made
 #pragma unroll
