@@ -98,8 +98,7 @@ struct DeltaSpan {
     const float *from;                  // states before
     float *to;                          // and after
 };
-constexpr int kVec = 512;               // floats: e^G |k|, scale e^G |q|, e^(G_63 - G) |k|, e^G_63; zeros
-constexpr int kZeros = 256;             // an operand of zeros
+constexpr int kVec = 256;               // floats: e^G |k|, scale e^G |q|, e^(G_63 - G) |k|, e^G_63
 
 template <class T, int KB> struct DeltaSizes {
     static constexpr size_t t = 3 * kLower * kFragment;
@@ -241,7 +240,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
         vec[128 + place_of(lane)] = lane < here ? apart(G2[kChunk - 1], G) * rk[lane] : 0.0f;
         if (lane == kChunk - 1)
             vec[192] = D;
-        *(v4f *)(vec + kZeros + 4 * lane) = v4f{};
     }
 
     // L and P, the lower triangle in tiles of 16 columns.  A lane has four of L's rows
@@ -408,18 +406,17 @@ constexpr int kProducts[4] = {0, 3, 5, 6};
 
 // What a wave reads of a chunk.  The first four waves, a tile of its rows each, carry
 // the state along; four others, beside them, make the outputs.
-template <class T, int KB> struct StateOperands {
+// Tiles 0 and 1 have one operand of a lower triangle (N = 1), 2 and 3 two.
+template <class T, int KB, int N> struct StateOperands {
     static constexpr int KP = kPlanes<T>, TW = (2 * KB + 3) / 4;
-    v8b k[KB][KP], t[2][3], kt[TW][2][KP];
+    v8b k[KB][KP], t[N][3], kt[TW][2][KP];
     typename T::raw v[4];
-    v4f k_row, w_row;
-    float D;
-    static constexpr int registers = 4 * (KB * KP + 6 + 2 * TW * KP) + 13;
+    static constexpr int registers = 4 * (KB * KP + 6 + 2 * TW * KP) + 4;
 };
-template <class T, int KB> struct OutOperands {
+template <class T, int KB, int N> struct OutOperands {
     static constexpr int KP = kPlanes<T>, PP = kOutLast<T> + 1;
-    v8b q[KB][KP], p[2][PP];
-    v4f q_row;
+    v8b q[KB][KP], p[N][PP];
+    v4f vec;
     static constexpr int registers = 4 * (KB * KP + 2 * PP) + 4;
 };
 // Two chunks are on their way where the registers of a wave (256) hold them.
@@ -452,6 +449,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
     using Sizes = DeltaSizes<T, KB>;
     constexpr int KP = kPlanes<T>, LAST = kOutLast<T>, PP = LAST + 1, TILES = 2 * KB, TW = (TILES + 3) / 4;
     __shared__ v8b Sf[KB][3][64], Rf[2][3][64], Uf[2][PP][64], Wf[2][3][64];
+    __shared__ v4f rows[2][64];                 // factors of rows of this chunk and the next
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), w = wave % 4;
     const int n16 = lane % 16, g = lane / 16;
     const Place pl = place_in(slices);
@@ -474,7 +472,8 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
     const uint32_t v_col = (uint32_t)(in ? col : dv - 1) * sizeof(raw);
     const size_t unit0 = (size_t)pl.bh * sp.count;
     const size_t key_unit0 = (size_t)(b * a.d.key_heads + key_head) * sp.count;
-    const uint32_t lane16 = lane * 16, row_at = (16 * w + 4 * g) * sizeof(float);
+    const uint32_t lane16 = lane * 16;
+    const int row4 = 4 * w + g;                 // of `rows`: this lane's four rows
     auto operand = [&](const char *base) { return *(const v8b *)(base + lane16); };
     auto vec_of = [&](int c) { return sp.vec + (unit0 + c - first) * Sizes::vec; };
     // This wave's rows of K (0) or Q (1).
@@ -496,22 +495,23 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                     x[kb][p] = operand(at + (kb * KP + p) * kFragment);
         }
     };
-    // Operands of a lower triangle.  Tiles 0 and 1 have nothing beyond the diagonal: zeros
-    // in the place of a second one, since a branch around its products loses the wait that
-    // reading the others' results needs.
-    auto load_lower = [&](const char *at, int c, auto &x) {
-        constexpr int P = sizeof(x[0]) / sizeof(v8b);
+    // Operands of a lower triangle.
+    auto load_lower = [&](const char *at, auto &x) {
+        constexpr int N = sizeof(x) / sizeof(x[0]), P = sizeof(x[0]) / sizeof(v8b);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < N; ++p)
 #pragma unroll
             for (int s = 0; s < P; ++s)
-                x[p][s] = operand(p == 1 && w < 2 ? vec_of(c) + kZeros * sizeof(float)
-                                                  : at + (size_t)(lower_of(w, p) * P + s) * kFragment);
+                x[p][s] = operand(at + (size_t)(lower_of(w, p) * P + s) * kFragment);
     };
 
-    if (wave < 4) {
+    // (Tiles with one and with two operands of a triangle go their own ways: a branch
+    // around some of a wave's products loses the wait that reading the others' results
+    // needs.)
+    auto carry = [&](auto operands) {
         // the state: this wave's tiles in registers, everyone's as operands in LDS
-        using Operands = StateOperands<T, KB>;
+        constexpr int N = decltype(operands)::value;
+        using Operands = StateOperands<T, KB, N>;
         const char *v_at = (const char *)a.v + (b * a.d.v_batch_stride + head * a.d.v_head_stride) * sizeof(raw);
         const uint32_t v_step = (uint32_t)a.d.v_step_stride * sizeof(raw);
         v4f S[TW];
@@ -542,12 +542,8 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 x.v[r] = *(const raw *)(at + ((uint32_t)(out_row + r < most ? out_row + r : most) * v_step + v_col));
-            x.k_row = *(const v4f *)(vec_of(c) + row_at);
         };
-        auto load_t = [&](Operands &x, int c) {
-            load_lower(sp.t + (unit0 + c - first) * Sizes::t, c, x.t);
-            x.w_row = *(const v4f *)(vec_of(c) + 512 + row_at);
-        };
+        auto load_t = [&](Operands &x, int c) { load_lower(sp.t + (unit0 + c - first) * Sizes::t, x.t); };
         auto load_kt = [&](Operands &x, int c) {
             const char *at = sp.kt + (key_unit0 + c - first) * Sizes::kt;
 #pragma unroll
@@ -559,7 +555,6 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                     for (int s = 0; s < KP; ++s)
                         x.kt[y][p][s] = operand(at + (size_t)((tile * 2 + p) * KP + s) * kFragment);
             }
-            x.D = *(const float *)(vec_of(c) + 768);
         };
         __builtin_amdgcn_s_setprio(3);
         if (first < last) {
@@ -582,11 +577,12 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                         for (int e = 0; e + p <= 2 && e < KP; ++e)
                             X[e + p > 0] = mfma(x.k[kb][e], s, X[e + p > 0]);
                     }
-                spread<3 * KB, KB * kProducts[KP], 2 * TW * KP + 1>();
+                spread<3 * KB, KB * kProducts[KP], 2 * TW * KP>();
+                const v4f k_row = rows[c % 2][row4];
                 float R[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    R[r] = kChunk * c + out_row + r < n ? T::load(x.v[r]) - x.k_row[r] * (X[1][r] + X[0][r]) : 0.0f;
+                    R[r] = kChunk * c + out_row + r < n ? T::load(x.v[r]) - k_row[r] * (X[1][r] + X[0][r]) : 0.0f;
                 const Planes<3, 4> r_out(R);
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
@@ -595,7 +591,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                 // the corrections
                 v4f u[2] = {};
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                for (int p = 0; p < N; ++p)
 #pragma unroll
                     for (int s = 0; s < 3; ++s) {
                         const v8b r = Rf[p][s][lane];
@@ -604,12 +600,13 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                             u[e + s > 0] = mfma(x.t[p][e], r, u[e + s > 0]);
                     }
                 load_kv(x, next);
-                spread<6, 12, KB * KP + 5>();
+                spread<3 * N, 6 * N, KB * KP + 4>();
+                const v4f w_row = rows[c % 2][32 + row4];
                 float U[4], W[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     U[r] = u[1][r] + u[0][r];
-                    W[r] = U[r] * x.w_row[r];
+                    W[r] = U[r] * w_row[r];
                 }
                 const Planes<3, 4> w_out(W);
                 const Planes<PP, 4> u_out(U);
@@ -634,12 +631,13 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                                 d[t][e + s > 0] = mfma(x.kt[t][p][e], f, d[t][e + s > 0]);
                     }
                 load_t(x, next);
-                spread<6, 2 * TW * kProducts[KP], 7>();
+                spread<6, 2 * TW * kProducts[KP], 3 * N>();
+                const float D = rows[c % 2][48][0];
 #pragma unroll
                 for (int t = 0; t < TW; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        S[t][r] = __builtin_fmaf(x.D, S[t][r], d[t][1][r] + d[t][0][r]);
+                        S[t][r] = __builtin_fmaf(D, S[t][r], d[t][1][r] + d[t][0][r]);
                 publish();
                 lds_barrier();
             });
@@ -652,64 +650,85 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
                 if (sp.to && in && at < dk)
                     sp.to[state_at + (int64_t)at * dv] = S[x][r];
             }
+    };
+
+    // the outputs, and the factors of rows brought into LDS
+    auto answer = [&](auto operands) {
+        constexpr int N = decltype(operands)::value;
+        using Operands = OutOperands<T, KB, N>;
+        constexpr int AHEAD = kAhead<Operands>;
+        auto load_q = [&](Operands &x, int c) {
+            load_rows(a.q, a.d.q_batch_stride, a.d.q_step_stride, a.d.q_head_stride, 1, c, x.q);
+        };
+        auto load_p = [&](Operands &x, int c) { load_lower(sp.p + (unit0 + c - first) * Sizes::p, x.p); };
+        // (of the chunk after c; every one of the four waves, so that none goes its own way)
+        auto load_vec = [&](Operands &x, int c) {
+            x.vec = *(const v4f *)(vec_of(c + 1 < last ? c + 1 : last - 1) + lane16);
+        };
+        if (first < last) {
+            rows[first % 2][lane] = *(const v4f *)(vec_of(first) + lane16);
+            along<AHEAD, Operands>(first, last, [&](Operands &x, int c) {
+                load_q(x, c);
+                load_p(x, c);
+                load_vec(x, c);
+            }, [&](Operands &x, Operands &, int c, int next) {
+                rows[(c + 1) % 2][lane] = x.vec;
+                load_vec(x, next);
+                const v4f q_row = rows[c % 2][16 + row4];
+                lds_barrier();
+                v4f Y[2] = {}, O[2] = {};       // Q S, while the corrections are made
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int p = 0; p <= LAST; ++p) {
+                        const v8b s = Sf[kb][p][lane];
+#pragma unroll
+                        for (int e = 0; e + p <= LAST && e < KP; ++e)
+                            Y[e + p > 0] = mfma(x.q[kb][e], s, Y[e + p > 0]);
+                    }
+                lds_barrier();
+#pragma unroll
+                for (int p = 0; p < N; ++p)
+#pragma unroll
+                    for (int s = 0; s < PP; ++s) {
+                        const v8b f = Uf[p][s][lane];
+#pragma unroll
+                        for (int e = 0; e + s <= LAST; ++e)
+                            O[e + s > 0] = mfma(x.p[p][e], f, O[e + s > 0]);
+                    }
+                load_q(x, next);
+                char *to = o_at + (size_t)c * kChunk * o_step;
+                const int start = kChunk * c;
+                raw out[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    out[r] = T::store(__builtin_fmaf(q_row[r], Y[1][r] + Y[0][r], O[1][r] + O[0][r]));
+                if (all_in && start + kChunk <= n) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (in && start + out_row + r < n)
+                            *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+                }
+                load_p(x, next);
+                lds_barrier();
+            });
+        }
+    };
+    if (wave < 4) {
+        if (w < 2)
+            carry(std::integral_constant<int, 1>{});
+        else
+            carry(std::integral_constant<int, 2>{});
         return;
     }
-
-    // the outputs
-    using Operands = OutOperands<T, KB>;
-    auto load_q = [&](Operands &x, int c) {
-        load_rows(a.q, a.d.q_batch_stride, a.d.q_step_stride, a.d.q_head_stride, 1, c, x.q);
-    };
-    auto load_p = [&](Operands &x, int c) {
-        load_lower(sp.p + (unit0 + c - first) * Sizes::p, c, x.p);
-        x.q_row = *(const v4f *)(vec_of(c) + 256 + row_at);
-    };
-    if (first < last)
-        along<kAhead<Operands>, Operands>(first, last, [&](Operands &x, int c) {
-            load_q(x, c);
-            load_p(x, c);
-        }, [&](Operands &x, Operands &, int c, int next) {
-            lds_barrier();
-            v4f Y[2] = {}, O[2] = {};           // Q S, while the corrections are made
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int p = 0; p <= LAST; ++p) {
-                    const v8b s = Sf[kb][p][lane];
-#pragma unroll
-                    for (int e = 0; e + p <= LAST && e < KP; ++e)
-                        Y[e + p > 0] = mfma(x.q[kb][e], s, Y[e + p > 0]);
-                }
-            load_q(x, next);
-            lds_barrier();
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-#pragma unroll
-                for (int s = 0; s < PP; ++s) {
-                    const v8b f = Uf[p][s][lane];
-#pragma unroll
-                    for (int e = 0; e + s <= LAST; ++e)
-                        O[e + s > 0] = mfma(x.p[p][e], f, O[e + s > 0]);
-                }
-            char *to = o_at + (size_t)c * kChunk * o_step;
-            const int start = kChunk * c;
-            raw out[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                out[r] = T::store(__builtin_fmaf(x.q_row[r], Y[1][r] + Y[0][r], O[1][r] + O[0][r]));
-            if (all_in && start + kChunk <= n) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (in && start + out_row + r < n)
-                        *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
-            }
-            load_p(x, next);
-            lds_barrier();
-        });
+    if (w < 2)
+        answer(std::integral_constant<int, 1>{});
+    else
+        answer(std::integral_constant<int, 2>{});
     // steps behind the last one of this span: zeros
     const int from = n > kChunk * first ? n : kChunk * first;
     const int64_t to = (int64_t)kChunk * (first + (int64_t)sp.count);
