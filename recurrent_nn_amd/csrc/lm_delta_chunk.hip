@@ -410,46 +410,51 @@ constexpr int kProducts[4] = {0, 3, 5, 6};
 template <class T, int KB, int N> struct StateOperands {
     static constexpr int KP = kPlanes<T>, TW = (2 * KB + 3) / 4;
     v8b k[KB][KP], t[N][3], kt[TW][2][KP];
-    typename T::raw v[4];
-    static constexpr int registers = 4 * (KB * KP + 6 + 2 * TW * KP) + 4;
+    static constexpr int registers = 4 * (KB * KP + 6 + 2 * TW * KP);
 };
-template <class T, int KB, int N> struct OutOperands {
+template <class T, int KB, int N, int NC> struct OutOperands {
     static constexpr int KP = kPlanes<T>, PP = kOutLast<T> + 1;
     v8b q[KB][KP], p[N][PP];
+    typedef uint32_t Four __attribute__((ext_vector_type(sizeof(typename T::raw))));    // values
     v4f vec;
-    static constexpr int registers = 4 * (KB * KP + 2 * PP) + 4;
+    Four v[NC];
+    static constexpr int registers = 4 * (KB * KP + 2 * PP) + 4 + NC * (int)sizeof(typename T::raw);
 };
 // Two chunks are on their way where the registers of a wave (256) hold them.
 template <class Operands> constexpr int kAhead = Operands::registers <= 90 ? 2 : 1;
 
 // f(operands of the chunk, of the one before it, chunk, the chunk whose operands take
-// its own's place) for each chunk of [first, last).
-template <int AHEAD, class Operands, class Load, class F>
-__device__ __forceinline__ void along(int first, int last, Load &&load, F &&f)
+// its own's place, whether all its steps are there for sure) for each chunk of [first,
+// last).
+template <int AHEAD, bool WHOLE, class Operands, class Load, class F>
+__device__ __forceinline__ void along(int first, int last, Operands (&x)[AHEAD], Load &&load, F &&f)
 {
-    Operands x[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
         load(x[i], first + i < last ? first + i : last - 1);
     lds_barrier();                              // (the state is published)
-    auto next = [&](int c) { return c + AHEAD < last ? c + AHEAD : last - 1; };
     int c = first;
-    for (; c + AHEAD <= last; c += AHEAD)       // (no way round a load: waits are by their number)
+    for (; c + AHEAD < last; c += AHEAD)        // (no way round a load: waits are by their number)
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
-            f(x[i], x[(i + AHEAD - 1) % AHEAD], c + i, next(c + i));
-    if (c < last)
-        f(x[0], x[AHEAD - 1], c, last - 1);
+            f(x[i], x[(i + AHEAD - 1) % AHEAD], c + i, c + i + AHEAD < last ? c + i + AHEAD : last - 1,
+              std::integral_constant<bool, WHOLE>{});
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (c + i < last)
+            f(x[i], x[(i + AHEAD - 1) % AHEAD], c + i, last - 1, std::false_type{});
 }
 
-template <class T, int KB, bool DIRECT>
+// NC tiles of 16 columns of the state a workgroup.
+template <class T, int KB, bool DIRECT, int NC>
 __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpan sp, uint32_t slices)
 {
     using raw = typename T::raw;
     using Sizes = DeltaSizes<T, KB>;
     constexpr int KP = kPlanes<T>, LAST = kOutLast<T>, PP = LAST + 1, TILES = 2 * KB, TW = (TILES + 3) / 4;
-    __shared__ v8b Sf[KB][3][64], Rf[2][3][64], Uf[2][PP][64], Wf[2][3][64];
+    __shared__ v8b Sf[NC][KB][3][64], Rf[NC][2][3][64], Uf[NC][2][PP][64], Wf[NC][2][3][64];
     __shared__ v4f rows[2][64];                 // factors of rows of this chunk and the next
+    __shared__ __attribute__((aligned(16))) raw Vs[kChunk][16 * NC];
     const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), w = wave % 4;
     const int n16 = lane % 16, g = lane / 16;
     const Place pl = place_in(slices);
@@ -458,8 +463,8 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
     if (b >= a.d.batch)
         return;
     const int n = delta_steps(a, b), steps = (int)a.d.steps;
-    const int dk = (int)a.d.key_dim, dv = (int)a.d.value_dim, col = (int)pl.at * 16 + n16;
-    const bool in = col < dv, all_in = (int)pl.at * 16 + 16 <= dv;
+    const int dk = (int)a.d.key_dim, dv = (int)a.d.value_dim, col0 = (int)pl.at * 16 * NC, col = col0 + n16;
+    const bool all_in = col0 + 16 * NC <= dv;
     const int64_t key_head = head / (a.d.heads / a.d.key_heads);
     const int first = (int)sp.first, all = (n + kChunk - 1) / kChunk;
     const int last = first + (int)sp.count < all ? first + (int)sp.count : all;     // chunks [first, last)
@@ -469,7 +474,7 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
     const int row = row_of(w, n16), out_row = row_of(w, 4 * g);
     char *o_at = (char *)a.o + (b * a.d.o_batch_stride + head * a.d.o_head_stride) * sizeof(raw);
     const uint32_t o_step = (uint32_t)a.d.o_step_stride * sizeof(raw);
-    const uint32_t v_col = (uint32_t)(in ? col : dv - 1) * sizeof(raw);
+    const uint32_t o_col = (uint32_t)col * sizeof(raw);
     const size_t unit0 = (size_t)pl.bh * sp.count;
     const size_t key_unit0 = (size_t)(b * a.d.key_heads + key_head) * sp.count;
     const uint32_t lane16 = lane * 16;
@@ -512,36 +517,34 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
         // the state: this wave's tiles in registers, everyone's as operands in LDS
         constexpr int N = decltype(operands)::value;
         using Operands = StateOperands<T, KB, N>;
-        const char *v_at = (const char *)a.v + (b * a.d.v_batch_stride + head * a.d.v_head_stride) * sizeof(raw);
-        const uint32_t v_step = (uint32_t)a.d.v_step_stride * sizeof(raw);
-        v4f S[TW];
+        v4f S[NC][TW];
         const int64_t state_at = (int64_t)pl.bh * dk * dv + col;
 #pragma unroll
-        for (int x = 0; x < TW; ++x)
+        for (int z = 0; z < NC; ++z)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int at = row_of(w * TW + x, 4 * g + r);
-                S[x][r] = sp.from && in && at < dk ? sp.from[state_at + (int64_t)at * dv] : 0.0f;
-            }
+            for (int x = 0; x < TW; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = row_of(w * TW + x, 4 * g + r);
+                    S[z][x][r] = sp.from && col + 16 * z < dv && at < dk
+                                     ? sp.from[state_at + (int64_t)at * dv + 16 * z] : 0.0f;
+                }
         auto publish = [&]() {
 #pragma unroll
-            for (int x = 0; x < TW; ++x) {
-                const int tile = w * TW + x;
-                const float s[4] = {S[x][0], S[x][1], S[x][2], S[x][3]};
-                const Planes<3, 4> out(s);
-                if (4 * TW == TILES || tile < TILES)
+            for (int z = 0; z < NC; ++z)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        out.put(p, (v4b *)&Sf[tile / 2][p][lane] + tile % 2);
-            }
+                for (int x = 0; x < TW; ++x) {
+                    const int tile = w * TW + x;
+                    const float s[4] = {S[z][x][0], S[z][x][1], S[z][x][2], S[z][x][3]};
+                    const Planes<3, 4> out(s);
+                    if (4 * TW == TILES || tile < TILES)
+#pragma unroll
+                        for (int p = 0; p < 3; ++p)
+                            out.put(p, (v4b *)&Sf[z][tile / 2][p][lane] + tile % 2);
+                }
         };
-        auto load_kv = [&](Operands &x, int c) {
+        auto load_k = [&](Operands &x, int c) {
             load_rows(a.k, a.d.k_batch_stride, a.d.k_step_stride, a.d.k_head_stride, 0, c, x.k);
-            const int most = n - 1 - kChunk * c;
-            const char *at = v_at + (size_t)c * kChunk * v_step;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                x.v[r] = *(const raw *)(at + ((uint32_t)(out_row + r < most ? out_row + r : most) * v_step + v_col));
         };
         auto load_t = [&](Operands &x, int c) { load_lower(sp.t + (unit0 + c - first) * Sizes::t, x.t); };
         auto load_kt = [&](Operands &x, int c) {
@@ -560,162 +563,222 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
         if (first < last) {
             publish();
             constexpr int AHEAD = kAhead<Operands>;
-            along<AHEAD, Operands>(first, last, [&](Operands &x, int c) {
-                load_kv(x, c);
+            Operands both[AHEAD];
+            along<AHEAD, true>(first, last, both, [&](Operands &x, int c) {
+                load_k(x, c);
                 load_t(x, c);
                 load_kt(x, c);
-            }, [&](Operands &x, Operands &before, int c, int next) {
+            }, [&](Operands &x, Operands &before, int c, int next, auto) {
                 // K S, and what the corrections solve for
                 load_kt(before, c + AHEAD - 1 < last ? c + AHEAD - 1 : last - 1);
-                v4f X[2] = {};
+                v4f X[NC][2] = {};
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const v8b s = Sf[kb][p][lane];
+                    for (int p = 0; p < 3; ++p)
 #pragma unroll
-                        for (int e = 0; e + p <= 2 && e < KP; ++e)
-                            X[e + p > 0] = mfma(x.k[kb][e], s, X[e + p > 0]);
-                    }
-                spread<3 * KB, KB * kProducts[KP], 2 * TW * KP>();
+                        for (int z = 0; z < NC; ++z) {
+                            const v8b s = Sf[z][kb][p][lane];
+#pragma unroll
+                            for (int e = 0; e + p <= 2 && e < KP; ++e)
+                                X[z][e + p > 0] = mfma(x.k[kb][e], s, X[z][e + p > 0]);
+                        }
+                spread<3 * KB * NC, KB * kProducts[KP] * NC, 2 * TW * KP>();
                 const v4f k_row = rows[c % 2][row4];
-                float R[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    R[r] = kChunk * c + out_row + r < n ? T::load(x.v[r]) - k_row[r] * (X[1][r] + X[0][r]) : 0.0f;
-                const Planes<3, 4> r_out(R);
+                for (int z = 0; z < NC; ++z) {
+                    float R[4];                 // (T has zeros for rows that are not there)
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    r_out.put(p, (v4b *)&Rf[w / 2][p][lane] + w % 2);
+                    for (int r = 0; r < 4; ++r)
+                        R[r] = __builtin_fmaf(-k_row[r], X[z][1][r] + X[z][0][r],
+                                              T::load(Vs[out_row + r][16 * z + n16]));
+                    const Planes<3, 4> r_out(R);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        r_out.put(p, (v4b *)&Rf[z][w / 2][p][lane] + w % 2);
+                }
                 lds_barrier();
                 // the corrections
-                v4f u[2] = {};
+                v4f u[NC][2] = {};
 #pragma unroll
                 for (int p = 0; p < N; ++p)
 #pragma unroll
-                    for (int s = 0; s < 3; ++s) {
-                        const v8b r = Rf[p][s][lane];
+                    for (int s = 0; s < 3; ++s)
 #pragma unroll
-                        for (int e = 0; e + s <= 2; ++e)
-                            u[e + s > 0] = mfma(x.t[p][e], r, u[e + s > 0]);
-                    }
-                load_kv(x, next);
-                spread<3 * N, 6 * N, KB * KP + 4>();
+                        for (int z = 0; z < NC; ++z) {
+                            const v8b r = Rf[z][p][s][lane];
+#pragma unroll
+                            for (int e = 0; e + s <= 2; ++e)
+                                u[z][e + s > 0] = mfma(x.t[p][e], r, u[z][e + s > 0]);
+                        }
+                load_k(x, next);
+                spread<3 * N * NC, 6 * N * NC, KB * KP>();
                 const v4f w_row = rows[c % 2][32 + row4];
-                float U[4], W[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    U[r] = u[1][r] + u[0][r];
-                    W[r] = U[r] * w_row[r];
+                for (int z = 0; z < NC; ++z) {
+                    float U[4], W[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        U[r] = u[z][1][r] + u[z][0][r];
+                        W[r] = U[r] * w_row[r];
+                    }
+                    const Planes<3, 4> w_out(W);
+                    const Planes<PP, 4> u_out(U);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        w_out.put(p, (v4b *)&Wf[z][w / 2][p][lane] + w % 2);
+#pragma unroll
+                    for (int p = 0; p < PP; ++p)
+                        u_out.put(p, (v4b *)&Uf[z][w / 2][p][lane] + w % 2);
                 }
-                const Planes<3, 4> w_out(W);
-                const Planes<PP, 4> u_out(U);
-#pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    w_out.put(p, (v4b *)&Wf[w / 2][p][lane] + w % 2);
-#pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    u_out.put(p, (v4b *)&Uf[w / 2][p][lane] + w % 2);
                 lds_barrier();
                 // the state
-                v4f d[TW][2] = {};
+                v4f d[NC][TW][2] = {};
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int s = 0; s < 3; ++s) {
-                        const v8b f = Wf[p][s][lane];
+                    for (int s = 0; s < 3; ++s)
 #pragma unroll
-                        for (int t = 0; t < TW; ++t)
+                        for (int z = 0; z < NC; ++z) {
+                            const v8b f = Wf[z][p][s][lane];
 #pragma unroll
-                            for (int e = 0; e + s <= 2 && e < KP; ++e)
-                                d[t][e + s > 0] = mfma(x.kt[t][p][e], f, d[t][e + s > 0]);
-                    }
+                            for (int t = 0; t < TW; ++t)
+#pragma unroll
+                                for (int e = 0; e + s <= 2 && e < KP; ++e)
+                                    d[z][t][e + s > 0] = mfma(x.kt[t][p][e], f, d[z][t][e + s > 0]);
+                        }
                 load_t(x, next);
-                spread<6, 2 * TW * kProducts[KP], 3 * N>();
+                spread<6 * NC, 2 * TW * kProducts[KP] * NC, 3 * N>();
                 const float D = rows[c % 2][48][0];
 #pragma unroll
-                for (int t = 0; t < TW; ++t)
+                for (int z = 0; z < NC; ++z)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        S[t][r] = __builtin_fmaf(D, S[t][r], d[t][1][r] + d[t][0][r]);
+                    for (int t = 0; t < TW; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            S[z][t][r] = __builtin_fmaf(D, S[z][t][r], d[z][t][1][r] + d[z][t][0][r]);
                 publish();
                 lds_barrier();
             });
         }
 #pragma unroll
-        for (int x = 0; x < TW; ++x)
+        for (int z = 0; z < NC; ++z)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int at = row_of(w * TW + x, 4 * g + r);
-                if (sp.to && in && at < dk)
-                    sp.to[state_at + (int64_t)at * dv] = S[x][r];
-            }
+            for (int x = 0; x < TW; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = row_of(w * TW + x, 4 * g + r);
+                    if (sp.to && col + 16 * z < dv && at < dk)
+                        sp.to[state_at + (int64_t)at * dv + 16 * z] = S[z][x][r];
+                }
     };
 
-    // the outputs, and the factors of rows brought into LDS
-    auto answer = [&](auto operands) {
+    // the outputs; values and factors of rows are brought into LDS.  WHOLE: all columns
+    // are there.  (Where the number of loads and stores under way depends on a branch, all
+    // of them are waited for: whole chunks have no such branch.)
+    auto answer = [&](auto operands, auto whole) {
         constexpr int N = decltype(operands)::value;
-        using Operands = OutOperands<T, KB, N>;
+        constexpr bool WHOLE = decltype(whole)::value;
+        using Operands = OutOperands<T, KB, N, NC>;
         constexpr int AHEAD = kAhead<Operands>;
+        const char *v_at = (const char *)a.v + (b * a.d.v_batch_stride + head * a.d.v_head_stride) * sizeof(raw);
+        const uint32_t v_step = (uint32_t)a.d.v_step_stride * sizeof(raw);
+        const int v_row = 16 * w + lane / 4, v_col = col0 + 4 * (lane % 4);
         auto load_q = [&](Operands &x, int c) {
             load_rows(a.q, a.d.q_batch_stride, a.d.q_step_stride, a.d.q_head_stride, 1, c, x.q);
         };
         auto load_p = [&](Operands &x, int c) { load_lower(sp.p + (unit0 + c - first) * Sizes::p, x.p); };
-        // (of the chunk after c; every one of the four waves, so that none goes its own way)
+        // Of the chunk after c.  (All factors by every one of the four waves, so that none
+        // goes its own way.)
         auto load_vec = [&](Operands &x, int c) {
             x.vec = *(const v4f *)(vec_of(c + 1 < last ? c + 1 : last - 1) + lane16);
         };
-        if (first < last) {
-            rows[first % 2][lane] = *(const v4f *)(vec_of(first) + lane16);
-            along<AHEAD, Operands>(first, last, [&](Operands &x, int c) {
-                load_q(x, c);
-                load_p(x, c);
-                load_vec(x, c);
-            }, [&](Operands &x, Operands &, int c, int next) {
-                rows[(c + 1) % 2][lane] = x.vec;
-                load_vec(x, next);
-                const v4f q_row = rows[c % 2][16 + row4];
-                lds_barrier();
-                v4f Y[2] = {}, O[2] = {};       // Q S, while the corrections are made
+        auto load_v = [&](Operands &x, int c) {
+            c = c + 1 < last ? c + 1 : last - 1;
+            const int most = n - 1 - kChunk * c;
+            const char *at = v_at + (size_t)c * kChunk * v_step;
+            const uint32_t row = (uint32_t)(v_row < most ? v_row : most) * v_step;
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int p = 0; p <= LAST; ++p) {
-                        const v8b s = Sf[kb][p][lane];
-#pragma unroll
-                        for (int e = 0; e + p <= LAST && e < KP; ++e)
-                            Y[e + p > 0] = mfma(x.q[kb][e], s, Y[e + p > 0]);
-                    }
-                lds_barrier();
-#pragma unroll
-                for (int p = 0; p < N; ++p)
-#pragma unroll
-                    for (int s = 0; s < PP; ++s) {
-                        const v8b f = Uf[p][s][lane];
-#pragma unroll
-                        for (int e = 0; e + s <= LAST; ++e)
-                            O[e + s > 0] = mfma(x.p[p][e], f, O[e + s > 0]);
-                    }
-                load_q(x, next);
-                char *to = o_at + (size_t)c * kChunk * o_step;
-                const int start = kChunk * c;
-                raw out[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    out[r] = T::store(__builtin_fmaf(q_row[r], Y[1][r] + Y[0][r], O[1][r] + O[0][r]));
-                if (all_in && start + kChunk <= n) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+            for (int z = 0; z < NC; ++z) {
+                const int at_col = v_col + 16 * z;
+                typename Operands::Four v = {};
+                if (WHOLE) {
+                    __builtin_memcpy(&v, at + (row + at_col * (uint32_t)sizeof(raw)), sizeof(v));
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (in && start + out_row + r < n)
-                            *(raw *)(to + ((out_row + r) * o_step + v_col)) = out[r];
+                    for (int j = 0; j < 4; ++j) {
+                        const int there = at_col + j < dv ? at_col + j : dv - 1;
+                        const uint32_t r = *(const raw *)(at + (row + there * (uint32_t)sizeof(raw)));
+                        v[j * sizeof(raw) / 4] |= sizeof(raw) == 4 ? r : r << 16 * (j % 2);
+                    }
                 }
-                load_p(x, next);
-                lds_barrier();
-            });
+                x.v[z] = v;
+            }
+        };
+        auto put_v = [&](const Operands &x) {
+#pragma unroll
+            for (int z = 0; z < NC; ++z)
+                *(typename Operands::Four *)&Vs[v_row][16 * z + 4 * (lane % 4)] = x.v[z];
+        };
+        // (Operands are replaced where these waves have nothing else to do: a load waits for
+        // those before it, and a barrier for the wave.)
+        auto chunk = [&](Operands &x, Operands &before, int c, int next, auto all_rows) {
+            rows[(c + 1) % 2][lane] = x.vec;
+            load_vec(x, next);
+            load_p(before, c + AHEAD - 1 < last ? c + AHEAD - 1 : last - 1);
+            const v4f q_row = rows[c % 2][16 + row4];
+            lds_barrier();
+            v4f Y[NC][2] = {}, O[NC][2] = {};   // Q S, while the corrections are made
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int p = 0; p <= LAST; ++p)
+#pragma unroll
+                    for (int z = 0; z < NC; ++z) {
+                        const v8b s = Sf[z][kb][p][lane];
+#pragma unroll
+                        for (int e = 0; e + p <= LAST && e < KP; ++e)
+                            Y[z][e + p > 0] = mfma(x.q[kb][e], s, Y[z][e + p > 0]);
+                    }
+            put_v(x);
+            load_v(x, next);
+            load_q(x, next);
+            lds_barrier();
+#pragma unroll
+            for (int y = 0; y < N; ++y)
+#pragma unroll
+                for (int s = 0; s < PP; ++s)
+#pragma unroll
+                    for (int z = 0; z < NC; ++z) {
+                        const v8b f = Uf[z][y][s][lane];
+#pragma unroll
+                        for (int e = 0; e + s <= LAST; ++e)
+                            O[z][e + s > 0] = mfma(x.p[y][e], f, O[z][e + s > 0]);
+                    }
+            char *to = o_at + (size_t)c * kChunk * o_step;
+            const int start = kChunk * c;
+#pragma unroll
+            for (int z = 0; z < NC; ++z)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const raw out = T::store(__builtin_fmaf(q_row[r], Y[z][1][r] + Y[z][0][r], O[z][1][r] + O[z][0][r]));
+                    if (decltype(all_rows)::value || (col + 16 * z < dv && start + out_row + r < n))
+                        *(raw *)(to + ((out_row + r) * o_step + o_col + 16 * z * (uint32_t)sizeof(raw))) = out;
+                }
+            lds_barrier();
+        };
+        if (first < last) {
+            Operands x[AHEAD];
+            load_vec(x[0], first - 1);
+            load_v(x[0], first - 1);
+            rows[first % 2][lane] = x[0].vec;
+            put_v(x[0]);
+            along<AHEAD, WHOLE>(first, last, x, [&](Operands &y, int c) {
+                load_vec(y, c);
+                load_v(y, c);
+                load_q(y, c);
+                load_p(y, c);
+            }, chunk);
         }
     };
     if (wave < 4) {
@@ -725,17 +788,26 @@ __global__ __launch_bounds__(512) void delta_chunks_kernel(DeltaArgs a, DeltaSpa
             carry(std::integral_constant<int, 2>{});
         return;
     }
-    if (w < 2)
-        answer(std::integral_constant<int, 1>{});
-    else
-        answer(std::integral_constant<int, 2>{});
+    if (all_in) {
+        if (w < 2)
+            answer(std::integral_constant<int, 1>{}, std::true_type{});
+        else
+            answer(std::integral_constant<int, 2>{}, std::true_type{});
+    } else {
+        if (w < 2)
+            answer(std::integral_constant<int, 1>{}, std::false_type{});
+        else
+            answer(std::integral_constant<int, 2>{}, std::false_type{});
+    }
     // steps behind the last one of this span: zeros
     const int from = n > kChunk * first ? n : kChunk * first;
     const int64_t to = (int64_t)kChunk * (first + (int64_t)sp.count);
     const int until = to < steps ? (int)to : steps;
-    if (in)
-        for (int t = from + (tid - 256) / 16; t < until; t += 16)
-            *(raw *)(o_at + (size_t)t * o_step + v_col) = 0;
+#pragma unroll
+    for (int z = 0; z < NC; ++z)
+        if (col + 16 * z < dv)
+            for (int t = from + (tid - 256) / 16; t < until; t += 16)
+                *(raw *)(o_at + (size_t)t * o_step + o_col + 16 * z * sizeof(raw)) = 0;
 }
 
 // The workspace of a span of `count` chunks, as its parts lie in it; then the
@@ -768,12 +840,19 @@ template <class T, int KB> static uint64_t span_of(const rnn_delta_desc &d, bool
     return most < 1 ? 1 : most < all ? most : all;
 }
 
+// Two tiles of columns a workgroup where one would be more workgroups than compute units.
+static bool wide_slices(const rnn_delta_desc &d)
+{
+    return d.key_dim <= 192 && d.batch * d.heads * ((d.value_dim + 15) / 16) > 256;
+}
+
 template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a, hipStream_t s)
 {
     const uint64_t all = chunks_of(a.d), span = span_of<T, KB>(a.d, DIRECT);
     const DeltaLayout l = layout_of<T, KB>(a.d, span, DIRECT);
     const uint64_t rounds = ((uint64_t)a.d.batch * a.d.heads + 7) / 8;
-    const uint64_t slices = ((uint64_t)a.d.value_dim + 15) / 16;
+    const bool wide = wide_slices(a.d);
+    const uint64_t slices = ((uint64_t)a.d.value_dim + (wide ? 31 : 15)) / (wide ? 32 : 16);
     if (!launchable(rounds * 8 * span, 256) || !launchable(rounds * 8 * slices, 512))
         return (int)hipErrorInvalidConfiguration;
     char *ws = (char *)a.workspace;
@@ -787,8 +866,12 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
         int rc = (int)hipGetLastError();
         if (rc)
             return rc;
-        delta_chunks_kernel<T, KB, DIRECT>
-            <<<dim3((uint32_t)(rounds * 8 * slices)), dim3(512), 0, s>>>(a, sp, (uint32_t)slices);
+        const dim3 grid((uint32_t)(rounds * 8 * slices)), block(512);
+        if (!wide)
+            delta_chunks_kernel<T, KB, DIRECT, 1><<<grid, block, 0, s>>>(a, sp, (uint32_t)slices);
+        if constexpr (KB <= 6)
+            if (wide)
+                delta_chunks_kernel<T, KB, DIRECT, 2><<<grid, block, 0, s>>>(a, sp, (uint32_t)slices);
         rc = (int)hipGetLastError();
         if (rc)
             return rc;
