@@ -118,6 +118,26 @@ __device__ __forceinline__ Place place_in(uint32_t each)
     return {i / each * 8 + blockIdx.x % 8, i % each};
 }
 
+// The sum of the lanes up to this one.
+__device__ __forceinline__ double sums_up_to(double v)
+{
+    auto with = [&](auto ctrl, auto rows) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        auto moved = [&](uint32_t half) {
+            return (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)half, decltype(ctrl)::value,
+                                                                   decltype(rows)::value, 0xF, false);
+        };
+        v += __builtin_bit_cast(double, moved((uint32_t)(u >> 32)) << 32 | moved((uint32_t)u));
+    };
+    with(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});   // from the lane 1 before
+    with(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});   // 2
+    with(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});   // 4
+    with(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});   // 8
+    with(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row 0 to 1, 2 to 3
+    with(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // rows 0, 1 to 2, 3
+    return v;
+}
+
 template <class T, int KB, bool DIRECT>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSpan sp)
 {
@@ -125,7 +145,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
     constexpr int KP = kPlanes<T>, PP = kOutLast<T> + 1, LDK = 32 * KB + 8, LDT = 68;
     using Sizes = DeltaSizes<T, KB>;
     __shared__ __attribute__((aligned(16))) __bf16 keys[KP][kChunk][LDK];
-    __shared__ __attribute__((aligned(16))) float Lt[kChunk][LDT], Tm[kChunk][LDT];    // L transposed; P, then T
+    // L transposed above the diagonal, (1 + L)^-1 on it and below
+    __shared__ __attribute__((aligned(16))) float M[kChunk][LDT];
     __shared__ float2 G2[kChunk];               // sums of log2 decays, and what float32 leaves of them
     __shared__ __attribute__((aligned(16))) float rates[kChunk], rk[kChunk], rq[kChunk];
     const int tid = threadIdx.x, lane = tid % 64, w = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -220,12 +241,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
         double sum = 0.0;
         if (a.g && lane < here)
             sum = log_decay(log_g, a.A != nullptr, a.A ? a.A[head] : 0.0f, a.dt_bias ? a.dt_bias[head] : 0.0f);
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double before = __shfl_up(sum, d);
-            sum += lane >= d ? before : 0.0;
-        }
-        sum *= 1.4426950408889634074;
+        sum = sums_up_to(sum) * 1.4426950408889634074;
         G2[lane] = {(float)sum, (float)(sum - (double)(float)sum)};
         rates[lane] = lane < here ? rate_of(beta, a.d.beta_sigmoid) : 0.0f;
     }
@@ -243,7 +259,8 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
     }
 
     // L and P, the lower triangle in tiles of 16 columns.  A lane has four of L's rows
-    // of a column, and (its operands in the other order) four of P's columns of a row.
+    // of a column, and (its operands in the other order) four of P's columns of a row,
+    // which are half of what a lane takes of an operand.
     {
         const int i0 = row_of(w, 4 * g);
         float2 Gi[4];
@@ -255,56 +272,49 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
         }
         const float2 Gq = G2[row];
         const float rqi = rq[row];
-        for (int c = 0; c < (w < 2 ? 2 : 4); ++c) {
-            v4f kc = {}, qc = {};
+        char *p_at = sp.p + unit * Sizes::p + (n16 + 16 * (g / 2)) * 16 + g % 2 * 8;
+        for (int half = 0; half < (w < 2 ? 1 : 2); ++half) {
+            v4f kc[2] = {}, qc[2] = {};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int p = 0; p < KP; ++p) {
-                    const v8b other = *(const v8b *)&keys[p][16 * c + n16][32 * kb + 8 * g];
+                for (int p = 0; p < KP; ++p)
 #pragma unroll
-                    for (int s = 0; s < KP; ++s)
-                        if (s + p <= 2) {
-                            kc = mfma(kf[kb][s], other, kc);
-                            qc = mfma(other, qf[kb][s], qc);
-                        }
+                    for (int y = 0; y < 2; ++y) {
+                        const v8b other = *(const v8b *)&keys[p][32 * half + 16 * y + n16][32 * kb + 8 * g];
+#pragma unroll
+                        for (int s = 0; s < KP; ++s)
+                            if (s + p <= 2) {
+                                kc[y] = mfma(kf[kb][s], other, kc[y]);
+                                qc[y] = mfma(other, qf[kb][s], qc[y]);
+                            }
+                    }
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int j = 32 * half + 16 * y + n16, j0 = 32 * half + 16 * y + 4 * g;
+                const float2 Gj = G2[j];
+                const float rj = rk[j];
+                v4f l;
+                float p[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    l[r] = j < i0 + r ? fi[r] * (apart(Gi[r], Gj) * rj) * kc[y][r] : 0.0f;
+                    p[r] = j0 + r <= row ? rqi * (apart(Gq, G2[j0 + r]) * rk[j0 + r]) * qc[y][r] : 0.0f;
                 }
-            const int j = 16 * c + n16, j0 = 16 * c + 4 * g;
-            const float2 Gj = G2[j];
-            const float rj = rk[j];
-            v4f l, p;
+                *(v4f *)&M[j][i0] = l;
+                const Planes<PP, 4> out(p);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                l[r] = j < i0 + r ? fi[r] * (apart(Gi[r], Gj) * rj) * kc[r] : 0.0f;
-                p[r] = j0 + r <= row ? rqi * (apart(Gq, G2[j0 + r]) * rk[j0 + r]) * qc[r] : 0.0f;
+                for (int s = 0; s < PP; ++s)
+                    out.put(s, p_at + (size_t)(lower_of(w, half) * PP + s) * kFragment + 32 * y * 16);
             }
-            *(v4f *)&Lt[j][i0] = l;
-            *(v4f *)&Tm[row][j0] = p;
         }
     }
     __syncthreads();
-    // operands of the lower triangles, eight columns of a row a lane
-    auto operands = [&](int item, auto &&values, char *to, auto planes_of) {
-        constexpr int P = decltype(planes_of)::value;
-        const int f = item / 64, l = item % 64;
-        const int tile = f < 2 ? f : (f + 2) / 2, p = f < 2 ? 0 : f % 2;
-        float x[8];
-        values(row_of(tile, l % 16), 32 * p + 8 * (l / 16), x);
-        const Planes<P, 8> out(x);
-        to += (size_t)f * P * kFragment + l * 16;
-#pragma unroll
-        for (int s = 0; s < P; ++s)
-            out.put(s, to + s * kFragment);
-    };
-    for (int item = tid; item < kLower * 64; item += 256)
-        operands(item, [&](int i, int j, float (&x)[8]) {
-            __builtin_memcpy(x, &Tm[i][j], 32);
-        }, sp.p + unit * Sizes::p, std::integral_constant<int, PP>{});
     // (1 + L)^-1: the blocks on the diagonal, a column a lane, each entry taken off all
     // below it
-    float t[16];
     {
         const int at = 16 * w;
+        float t[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             t[i] = i == n16 ? 1.0f : 0.0f;
@@ -313,17 +323,15 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
             float l[16];
 #pragma unroll
             for (int i = (k + 1) / 4 * 4; i < 16; i += 4)
-                __builtin_memcpy(&l[i], &Lt[at + k][at + i], 16);
+                __builtin_memcpy(&l[i], &M[at + k][at + i], 16);
 #pragma unroll
             for (int i = k + 1; i < 16; ++i)
                 t[i] = __builtin_fmaf(-l[i], t[k], t[i]);
         }
-    }
-    __syncthreads();                            // (P has been read)
+        // (the wave alone has this block)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const float v = g == 0 ? t[r] : g == 1 ? t[4 + r] : g == 2 ? t[8 + r] : t[12 + r];
-        Tm[16 * w + 4 * g + r][16 * w + n16] = v;
+        for (int r = 0; r < 4; ++r)
+            M[at + 4 * g + r][at + n16] = g == 0 ? t[r] : g == 1 ? t[4 + r] : g == 2 ? t[8 + r] : t[12 + r];
     }
     // and those below: T_ij = -T_ii sum_k L_ik T_kj
 #pragma unroll
@@ -336,27 +344,36 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
             for (int k = 0; k < far; ++k)
 #pragma unroll
                 for (int s = 0; s < 4; ++s)
-                    x = mfma(Lt[j + 16 * k + 4 * g + s][i + n16], Tm[j + 16 * k + 4 * g + s][j + n16], x);
+                    x = mfma(M[j + 16 * k + 4 * g + s][i + n16], M[j + 16 * k + 4 * g + s][j + n16], x);
             float own[4];
-            __builtin_memcpy(own, &Tm[i + n16][i + 4 * g], 16);
+            __builtin_memcpy(own, &M[i + n16][i + 4 * g], 16);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 y = mfma(own[s], x[s], y);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                Tm[i + 4 * g + r][j + n16] = -y[r];
+                M[i + 4 * g + r][j + n16] = -y[r];
         }
     }
     __syncthreads();
-    for (int item = tid; item < kLower * 64; item += 256)
-        operands(item, [&](int i, int j, float (&x)[8]) {
-            float rate[8];
-            __builtin_memcpy(x, &Tm[i][j], 32);
-            __builtin_memcpy(rate, &rates[j], 32);
+    // its operands with the rates, four columns of a row (half of what a lane takes) a time
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                x[e] = j + e <= i ? x[e] * rate[e] : 0.0f;
-        }, sp.t + unit * Sizes::t, std::integral_constant<int, 3>{});
+    for (int item = tid; item < 2 * kLower * 64; item += 256) {
+        const int f = item / 128, l = item / 2 % 64;
+        const int tile = f < 2 ? f : (f + 2) / 2, p = f < 2 ? 0 : f % 2;
+        const int i = row_of(tile, l % 16), j = 32 * p + 8 * (l / 16) + 4 * (item % 2);
+        float x[4], rate[4];
+        __builtin_memcpy(x, &M[i][j], 16);
+        __builtin_memcpy(rate, &rates[j], 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = j + e <= i ? x[e] * rate[e] : 0.0f;
+        const Planes<3, 4> out(x);
+        char *to = sp.t + unit * Sizes::t + (size_t)f * 3 * kFragment + l * 16 + item % 2 * 8;
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+            out.put(s, to + s * kFragment);
+    }
     // K transposed: eight steps of a row of the state a lane
     if (head % each == 0)
         for (int item = tid; item < 4 * KB * 64; item += 256) {
