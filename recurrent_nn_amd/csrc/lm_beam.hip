@@ -282,13 +282,15 @@ __device__ __forceinline__ double key_double(uint64_t u)
 constexpr uint32_t kMostLists = 512;
 
 // The beams of a request together; `lists`: segments of all beams, up to
-// kMostLists or one a beam, each with its first `keep` entries in order.
+// kMostLists, each with its first `keep` entries in order.
 __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t segments)
 {
     constexpr uint32_t LIST = 512;
     __shared__ double base[RNN_BEAM_MAX];           // what a beam's candidates have beside x
     __shared__ uint8_t kind[RNN_BEAM_MAX];          // 0: dead, 1: runs, 2: finished
     __shared__ uint64_t ends[kMostLists], least;
+    __shared__ Total sums[kMostLists];
+    __shared__ float most[RNN_BEAM_MAX];
     __shared__ Candidate list[LIST], sorted[RNN_BEAM_MAX];
     __shared__ uint32_t count;
     const uint32_t tid = threadIdx.x, keep = (uint32_t)a.d.keep, beams = (uint32_t)a.d.beams;
@@ -299,33 +301,46 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
     const Total *totals = (const Total *)((const uint64_t *)a.workspace +
                                           (int64_t)gridDim.x * beams * segments * keep) +
                           first_row * segments;
+    const uint32_t all = lists * keep;
+    const uint64_t my_key = tid < all ? keys[tid] : 0;      // (on its way while the sums are joined)
     if (tid == 0) {
         count = 0;
         least = 0;
+    }
+    // every segment's sum by itself, then the beams': exponentials are long in float64
+    for (uint32_t i = tid; i < lists; i += 256) {
+        const int64_t row = first_row + i / segments;
+        sums[i] = beam_runs(a, row) ? totals[i] : Total{0.0, kLow};
     }
     if (tid < beams) {
         const int64_t row = first_row + tid;
         const float score = a.scores[row];
         base[tid] = score;
-        kind[tid] = 0;
-        if (a.finished && a.finished[row]) {
-            kind[tid] = score - score == 0.0f ? 2 : 0;
-        } else if (score - score == 0.0f) {
-            Total p = totals[tid * segments];
-            for (uint32_t s = 1; s < segments; ++s)
-                p.m = __builtin_fmaxf(p.m, totals[tid * segments + s].m);
-            double sum = 0.0;
-            for (uint32_t s = 0; s < segments; ++s) {
-                Total o = totals[tid * segments + s];
-                o.rebase(p.m);
-                sum += o.sum;
-            }
-            const double c = (double)score - ((double)p.m + log(sum));
-            if (c - c == 0.0) {
-                base[tid] = c;
-                kind[tid] = 1;
-            }
+        kind[tid] = score - score == 0.0f ? a.finished && a.finished[row] ? 2 : 1 : 0;
+    }
+    __syncthreads();
+    if (segments > 1) {
+        if (tid < beams) {
+            float m = kLow;
+            for (uint32_t s = 0; s < segments; ++s)
+                m = __builtin_fmaxf(m, sums[tid * segments + s].m);
+            most[tid] = m;
         }
+        __syncthreads();
+        for (uint32_t i = tid; i < lists; i += 256) {
+            Total o = sums[i];
+            o.rebase(most[i / segments]);
+            sums[i] = o;
+        }
+        __syncthreads();
+    }
+    if (tid < beams && kind[tid] == 1) {
+        double sum = 0.0;
+        for (uint32_t s = 0; s < segments; ++s)
+            sum += sums[tid * segments + s].sum;
+        const double c = base[tid] - ((double)sums[tid * segments].m + log(sum));
+        base[tid] = c;
+        kind[tid] = c - c == 0.0;
     }
     __syncthreads();
     // entry e of list l
@@ -333,7 +348,7 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
         const uint32_t beam = l / segments;
         const uint64_t row = beam * V, none = double_key(-(double)__builtin_inff());
         if (kind[beam] == 1) {
-            const uint64_t key = keys[(uint64_t)l * keep + e];
+            const uint64_t key = l * keep + e == tid ? my_key : keys[(uint64_t)l * keep + e];
             if (key == 0)
                 return Candidate{0, ~0ull};
             return Candidate{double_key(base[beam] + (double)key_value(key)), row + key_index(key)};
@@ -351,8 +366,7 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
     // If `need` lists have j + 1 candidates at or above a value each, and need (j + 1)
     // >= keep, then nothing below it counts.  With need about half of the lists, few
     // more than `keep` are left to order.
-    const uint32_t all = lists * keep;
-    if (all > 128 && lists <= kMostLists) {
+    if (all > 128) {
         uint32_t j = 0;
         while (j + 1 < keep && (keep + j) / (j + 1) > (lists + 1) / 2)
             ++j;

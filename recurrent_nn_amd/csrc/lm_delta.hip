@@ -4,8 +4,8 @@
 //   S = e^a S;  u = b (v - S^T k);  S = S + k u^T;  o = scale S^T q
 //
 // A state's columns are independent of each other.  A wave keeps 32 of them, all
-// rows, in registers: lane 8 g + c has columns 4 c to 4 c + 3 of the rows of group
-// g, so that a load covers whole 128-byte lines.  With D = e^a, k^T S and q^T S of
+// rows, in registers: lane 8 g + c has columns 4 c to 4 c + 3 of a quarter of each
+// 32 rows, so that a load covers whole 128-byte lines.  With D = e^a, k^T S and q^T S of
 // the state before the step are summed together, one reduction over the groups a
 // step:  u = b (v - D k^T S),  o = scale (D q^T S + (q . k) u),  S = D S + k u^T.
 // Norms of q and k are factors of these sums, and come with the same reduction.
@@ -38,21 +38,23 @@ __global__ __launch_bounds__(256) void delta_steps_kernel(DeltaArgs a, uint32_t 
     const int64_t b = (int64_t)(bh / heads), head = (int64_t)(bh % heads);
     if (b >= a.d.batch)
         return;
-    const int dk = (int)a.d.key_dim, dv = (int)a.d.value_dim, row0 = (int)group * NI;
+    const int dk = (int)a.d.key_dim, dv = (int)a.d.value_dim, row0 = (int)group * 4;
     const int tile = (int)(id % tiles) * 32, col = tile + 4 * (int)c;
     const bool whole = tile + 32 <= dv;         // the wave's columns are all there
     const int steps = (int)a.d.steps, n = delta_steps(a, b);
     const int64_t key_head = head / (heads / a.d.key_heads);
 
     float S[NI][4];
-    const int64_t state_at = ((int64_t)bh * dk + row0) * dv + col;
+    // register i has row 32 (i / 4) + 4 group + i % 4: four loads cover 32 rows
+    auto row_of = [&](int i) { return 32 * (i / 4) + row0 + i % 4; };
+    const int64_t state_at = (int64_t)bh * dk * dv + col;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             S[i][j] = 0.0f;
-        if (a.state_in && (FULL || row0 + i < dk)) {
-            const float *p = a.state_in + state_at + (int64_t)i * dv;
+        if (a.state_in && (FULL || row_of(i) < dk)) {
+            const float *p = a.state_in + state_at + (int64_t)row_of(i) * dv;
             if (whole) {
                 __builtin_memcpy(S[i], p, 16);
             } else {
@@ -79,12 +81,14 @@ __global__ __launch_bounds__(256) void delta_steps_kernel(DeltaArgs a, uint32_t 
     auto rows = [&](const raw *p) {
         Pack<T, NI> r;
         if (FULL) {
-            r = load_pack<T, NI>(p + row0);
+#pragma unroll
+            for (int i = 0; i < NI; i += 4)
+                __builtin_memcpy(&r.v[i], p + row_of(i), 4 * sizeof(raw));
         } else {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const raw x = p[row0 + i < dk ? row0 + i : dk - 1];
-                r.v[i] = row0 + i < dk ? x : (raw)0;
+                const raw x = p[row_of(i) < dk ? row_of(i) : dk - 1];
+                r.v[i] = row_of(i) < dk ? x : (raw)0;
             }
         }
         return r;
@@ -177,8 +181,8 @@ __global__ __launch_bounds__(256) void delta_steps_kernel(DeltaArgs a, uint32_t 
         return;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-        if (FULL || row0 + i < dk) {
-            float *p = a.state_out + state_at + (int64_t)i * dv;
+        if (FULL || row_of(i) < dk) {
+            float *p = a.state_out + state_at + (int64_t)row_of(i) * dv;
             if (whole) {
                 __builtin_memcpy(p, S[i], 16);
             } else {

@@ -30,9 +30,34 @@ template <int L> __device__ __forceinline__ float lanes_sum(float v)
     return v;
 }
 
+// Pack i of a group of `dim` elements: those from 8 i on.  Every load is unconditional:
+// packs beyond the end are the last one again, and where dim is no multiple of 8 the last
+// one is loaded from an earlier start.  The first `skip` elements are not its own.
+// WHOLE: dim is a multiple of 8; SHORT: below 8, one pack with its elements at its end.
+enum Shape { WHOLE, ODD, SHORT };
+template <class T> struct Part8 {
+    Pack<T, 8> v;
+    int start, skip;
+};
+template <class T, Shape S> __device__ __forceinline__ Part8<T> part_of(const typename T::raw *p, int i, int dim)
+{
+    Part8<T> r;
+    r.start = 8 * i < dim - 8 ? 8 * i : dim - 8;
+    r.skip = 8 * i - r.start;
+    if (S != SHORT) {
+        r.v = load_pack<T, 8>(p + r.start);
+    } else {
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            r.v.v[v] = p[r.start + v > 0 ? r.start + v : 0];
+        r.skip = i == 0 ? -r.start : 8;
+    }
+    return r;
+}
+
 // THREADS share a group; a thread's k-th pack is pack threadIdx + THREADS k of 8
 // elements.
-template <class T, int THREADS, int KEEP>
+template <class T, int THREADS, int KEEP, Shape S>
 __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(NormArgs a)
 {
     using raw = typename T::raw;
@@ -46,49 +71,42 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(Nor
     const raw *x = (const raw *)a.x + row * a.d.x_row_stride + group * a.d.x_group_stride;
     const raw *z = a.z ? (const raw *)a.z + row * a.d.z_row_stride + group * a.d.z_group_stride : x;
     raw *y = (raw *)a.y + row * a.d.y_row_stride + group * a.d.y_group_stride;
-    const float *w = a.weight + group * a.d.weight_group_stride;
+    const uint32_t *w = (const uint32_t *)a.weight + group * a.d.weight_group_stride;
     const int dim = (int)a.d.dim, packs = (dim + 7) / 8;
     const bool gated = a.z != nullptr, first = a.d.gate_first;
 
-    auto pack = [&](const raw *p, int i) {
-        Pack<T, 8> r{};
-        if (8 * i + 8 <= dim) {
-            r = load_pack<T, 8>(p + 8 * i);
-        } else {
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-                if (8 * i + v < dim)
-                    r.v[v] = p[8 * i + v];
-        }
-        return r;
-    };
-    auto value = [&](const Pack<T, 8> &p, const Pack<T, 8> &g, int v) {
-        const float f = T::load(p.v[v]);
-        return first ? f * silu(T::load(g.v[v])) : f;
-    };
-    float sum = 0.0f;
-    auto add = [&](const Pack<T, 8> &p, const Pack<T, 8> &g) {
-        float f[8];
+    using Part = Part8<T>;
+    auto at = [&](const raw *p, int i) { return part_of<T, S>(p, i, dim); };
+    // x, or x silu(z), of a pack
+    auto values = [&](const Part &p, const Part &g, float (&f)[8]) {
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
-            f[v] = value(p, g, v);
-            f[v] *= f[v];
+            f[v] = T::load(p.v.v[v]);
+            if (first)
+                f[v] *= silu(T::load(g.v.v[v]));
         }
-        sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
     };
-    Pack<T, 8> keep[KEEP], gate[KEEP];
+    float sum = 0.0f;
+    auto add = [&](const Part &p, const Part &g) {
+        float f[8];
+        values(p, g, f);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            f[v] = S == WHOLE || v >= p.skip ? f[v] * f[v] : 0.0f;
+        const float some = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        sum += S != WHOLE || p.skip == 0 ? some : 0.0f;
+    };
+    Part keep[KEEP], gate[KEEP];
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
-        keep[k] = pack(x, lane + THREADS * k);
-        gate[k] = keep[k];
-        if (gated)
-            gate[k] = pack(z, lane + THREADS * k);
+        keep[k] = at(x, lane + THREADS * k);
+        gate[k] = gated ? at(z, lane + THREADS * k) : keep[k];
     }
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
         add(keep[k], gate[k]);
     for (int i = lane + THREADS * KEEP; i < packs; i += THREADS)
-        add(pack(x, i), pack(z, i));
+        add(at(x, i), at(z, i));
     sum = lanes_sum<THREADS < 64 ? THREADS : 64>(sum);
     if (THREADS > 64) {
         if (threadIdx.x % 64 == 0)
@@ -100,30 +118,40 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(Nor
             sum += part[i];
     }
     const float r = 1.0f / sqrtf(sum / (float)dim + a.d.eps);
-    auto put = [&](int i, const Pack<T, 8> &p, const Pack<T, 8> &g) {
-        auto one = [&](int v, float weight) {
-            const float f = value(p, g, v) * r * weight;
-            return T::store(gated && !first ? f * silu(T::load(g.v[v])) : f);
-        };
-        if (8 * i + 8 <= dim) {
-            const Pack<F32, 8> weight = load_pack<F32, 8>((const uint32_t *)w + 8 * i);
-            Pack<T, 8> out;
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-                out.v[v] = one(v, F32::load(weight.v[v]));
-            store_pack<T, 8>(y + 8 * i, out);
+    auto put = [&](const Part &p, const Part &g) {
+        if (p.skip >= 8)
+            return;
+        float f[8], weight[8];
+        values(p, g, f);
+        if (S != SHORT) {
+            __builtin_memcpy(weight, w + p.start, sizeof(weight));
         } else {
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-                if (8 * i + v < dim)
-                    y[8 * i + v] = one(v, w[8 * i + v]);
+                weight[v] = __uint_as_float(w[p.start + v > 0 ? p.start + v : 0]);
+        }
+        Pack<T, 8> out;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            float o = f[v] * r * weight[v];
+            if (gated && !first)
+                o *= silu(T::load(g.v.v[v]));
+            out.v[v] = T::store(o);
+        }
+        if (S == WHOLE || p.skip == 0) {
+            store_pack<T, 8>(y + p.start, out);
+        } else {
+#pragma unroll
+            for (int v = 1; v < 8; ++v)
+                if (v >= p.skip)
+                    y[p.start + v] = out.v[v];
         }
     };
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
-        put(lane + THREADS * k, keep[k], gate[k]);
+        put(keep[k], gate[k]);
     for (int i = lane + THREADS * KEEP; i < packs; i += THREADS)
-        put(i, pack(x, i), pack(z, i));
+        put(at(x, i), at(z, i));
 }
 
 template <class T, int THREADS, int KEEP> static int norm_groups_go(const NormArgs &a, hipStream_t s)
@@ -132,7 +160,13 @@ template <class T, int THREADS, int KEEP> static int norm_groups_go(const NormAr
     const uint64_t blocks = ((uint64_t)a.d.rows * a.d.groups + EACH - 1) / EACH;
     if ((__int128)a.d.rows * a.d.groups > 0xFFFFFFFFu || !launchable(blocks, THREADS * EACH))
         return (int)hipErrorInvalidConfiguration;
-    norm_kernel<T, THREADS, KEEP><<<dim3((uint32_t)blocks), dim3(THREADS * EACH), 0, s>>>(a);
+    const dim3 grid((uint32_t)blocks), block(THREADS * EACH);
+    if (a.d.dim % 8 == 0)
+        norm_kernel<T, THREADS, KEEP, WHOLE><<<grid, block, 0, s>>>(a);
+    else if (THREADS > 4 || a.d.dim >= 8)
+        norm_kernel<T, THREADS, KEEP, ODD><<<grid, block, 0, s>>>(a);
+    else
+        norm_kernel<T, 4, 1, SHORT><<<grid, block, 0, s>>>(a);
     return (int)hipGetLastError();
 }
 
@@ -140,8 +174,12 @@ template <class T> static int norm_go(const NormArgs &a, hipStream_t s)
 {
     if (a.d.dim <= 32)
         return norm_groups_go<T, 4, 1>(a, s);
+    if (a.d.dim <= 128)
+        return norm_groups_go<T, 16, 1>(a, s);
     if (a.d.dim <= 256)
         return norm_groups_go<T, 16, 2>(a, s);
+    if (a.d.dim <= 512)
+        return norm_groups_go<T, 64, 1>(a, s);
     if (a.d.dim <= 2048)
         return norm_groups_go<T, 64, 4>(a, s);
     return a.d.dim <= 8192 ? norm_groups_go<T, 256, 4>(a, s) : norm_groups_go<T, 1024, 4>(a, s);
