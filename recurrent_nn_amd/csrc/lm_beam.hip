@@ -38,30 +38,6 @@ __device__ __forceinline__ bool beam_runs(const BeamArgs &a, int64_t row)
     return s - s == 0.0f && !(a.finished && a.finished[row]);
 }
 
-// The parts of a workgroup's 256 threads together, in every thread.
-__device__ __forceinline__ Total over_workgroup(Total p, Total (&parts)[4])
-{
-    p.rebase(value_of(wave_max(value_key(p.m))));
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        p.sum += __shfl_xor(p.sum, d);
-    if (threadIdx.x % 64 == 0)
-        parts[threadIdx.x / 64] = p;
-    __syncthreads();
-    Total all = parts[0];
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-        all.m = __builtin_fmaxf(all.m, parts[i].m);
-    all.sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        Total o = parts[i];
-        o.rebase(all.m);
-        all.sum += o.sum;
-    }
-    return all;
-}
-
 // One segment of a beam's row: packs [first, last) of 8 entries.  A thread takes
 // every 256th pack, U at a time: the loads of a batch are in flight while the one
 // before is summed.
@@ -75,7 +51,7 @@ template <class T> __global__ __launch_bounds__(256) void beam_rows_kernel(BeamA
     __shared__ float most[PARTS][256];
     __shared__ uint32_t count, bounds[4];
     __shared__ uint16_t items[256];
-    __shared__ Total parts[4];
+    __shared__ uint8_t finite[4];
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const int64_t row = blockIdx.x / segments;
     const uint32_t segment = blockIdx.x % segments;
@@ -175,16 +151,15 @@ template <class T> __global__ __launch_bounds__(256) void beam_rows_kernel(BeamA
         one(f);
         top_of_all = __builtin_fmaxf(top_of_all, f_rest);
     }
-    p = over_workgroup(p, parts);
-
+    // a wave's lanes have the same m
+    p.sum = sums_up_to(p.sum);
     const int top = a.d.keep;
     uint64_t *keys = (uint64_t *)a.workspace + (int64_t)blockIdx.x * top;
-    Total *out = (Total *)((uint64_t *)a.workspace + (int64_t)gridDim.x * top) + blockIdx.x;
-    if (tid == 0)
-        *out = p;
-    // NaN or infinite entries: the beam has no distribution, its entries do not count
-    if (!(p.sum < (double)__builtin_inff()))
-        return;
+    Total *out = (Total *)((uint64_t *)a.workspace + (int64_t)gridDim.x * top) + 4 * (int64_t)blockIdx.x;
+    if (lane == 63) {
+        out[wave] = p;
+        finite[wave] = p.sum < (double)__builtin_inff();
+    }
     Best best;
     best.begin(list, sorted, &count, top);
     // The bound, to 16 bits: the largest t that enough lanes of each wave reach.
@@ -199,6 +174,9 @@ template <class T> __global__ __launch_bounds__(256) void beam_rows_kernel(BeamA
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         t = bounds[i] < t ? bounds[i] : t;
+    // NaN or infinite entries: the beam has no distribution, its entries do not count
+    if (!(finite[0] && finite[1] && finite[2] && finite[3]))
+        return;
     // (cut to 16 bits, -inf lies below every number's key)
     const float edge = t < value_key(kLow) ? -__builtin_inff() : value_of(t);
     if (batches > 0)
@@ -289,7 +267,7 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
     __shared__ double base[RNN_BEAM_MAX];           // what a beam's candidates have beside x
     __shared__ uint8_t kind[RNN_BEAM_MAX];          // 0: dead, 1: runs, 2: finished
     __shared__ uint64_t ends[kMostLists], least;
-    __shared__ Total sums[kMostLists];
+    __shared__ Total sums[4 * kMostLists];
     __shared__ float most[RNN_BEAM_MAX];
     __shared__ Candidate list[LIST], sorted[RNN_BEAM_MAX];
     __shared__ uint32_t count;
@@ -300,18 +278,32 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
     const uint64_t *keys = (const uint64_t *)a.workspace + first_row * segments * keep;
     const Total *totals = (const Total *)((const uint64_t *)a.workspace +
                                           (int64_t)gridDim.x * beams * segments * keep) +
-                          first_row * segments;
+                          first_row * segments * 4;
     const uint32_t all = lists * keep;
-    const uint64_t my_key = tid < all ? keys[tid] : 0;      // (on its way while the sums are joined)
+    // If `need` lists have j + 1 candidates at or above a value each, and need (j + 1)
+    // >= keep, then nothing below it counts.  With need about half of the lists, few
+    // more than `keep` are left to order.
+    uint32_t j = 0;
+    while (j + 1 < keep && (keep + j) / (j + 1) > (lists + 1) / 2)
+        ++j;
+    const uint32_t need = (keep + j) / (j + 1);
+    // (keys that come while the sums are joined: the first ones, and those of `ends`)
+    constexpr uint32_t FIRST = 4;
+    uint64_t my_key[FIRST], end_key[kMostLists / 256];
+#pragma unroll
+    for (uint32_t i = 0; i < FIRST; ++i)
+        my_key[i] = keys[tid + 256 * i < all ? tid + 256 * i : 0];
+#pragma unroll
+    for (uint32_t i = 0; i < kMostLists / 256; ++i)
+        end_key[i] = keys[tid + 256 * i < lists ? (tid + 256 * i) * keep + j : 0];
     if (tid == 0) {
         count = 0;
         least = 0;
     }
-    // every segment's sum by itself, then the beams': exponentials are long in float64
-    for (uint32_t i = tid; i < lists; i += 256) {
-        const int64_t row = first_row + i / segments;
-        sums[i] = beam_runs(a, row) ? totals[i] : Total{0.0, kLow};
-    }
+    // every wave's sum by itself, then the beams': exponentials are long in float64
+    const uint32_t waves = 4 * segments, parts = beams * waves;
+    for (uint32_t i = tid; i < parts; i += 256)
+        sums[i] = beam_runs(a, first_row + i / waves) ? totals[i] : Total{0.0, kLow};
     if (tid < beams) {
         const int64_t row = first_row + tid;
         const float score = a.scores[row];
@@ -319,36 +311,39 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
         kind[tid] = score - score == 0.0f ? a.finished && a.finished[row] ? 2 : 1 : 0;
     }
     __syncthreads();
-    if (segments > 1) {
-        if (tid < beams) {
-            float m = kLow;
-            for (uint32_t s = 0; s < segments; ++s)
-                m = __builtin_fmaxf(m, sums[tid * segments + s].m);
-            most[tid] = m;
-        }
-        __syncthreads();
-        for (uint32_t i = tid; i < lists; i += 256) {
-            Total o = sums[i];
-            o.rebase(most[i / segments]);
-            sums[i] = o;
-        }
-        __syncthreads();
+    if (tid < beams) {
+        float m[4] = {kLow, kLow, kLow, kLow};  // (waves is a multiple of 4)
+#pragma unroll 4
+        for (uint32_t s = 0; s < waves; s += 4)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                m[v] = __builtin_fmaxf(m[v], sums[tid * waves + s + v].m);
+        most[tid] = __builtin_fmaxf(__builtin_fmaxf(m[0], m[1]), __builtin_fmaxf(m[2], m[3]));
     }
+    __syncthreads();
+    for (uint32_t i = tid; i < parts; i += 256) {
+        Total o = sums[i];
+        o.rebase(most[i / waves]);
+        sums[i].sum = o.sum;
+    }
+    __syncthreads();
     if (tid < beams && kind[tid] == 1) {
-        double sum = 0.0;
-        for (uint32_t s = 0; s < segments; ++s)
-            sum += sums[tid * segments + s].sum;
-        const double c = base[tid] - ((double)sums[tid * segments].m + log(sum));
+        double sum[4] = {};
+#pragma unroll 4
+        for (uint32_t s = 0; s < waves; s += 4)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                sum[v] += sums[tid * waves + s + v].sum;
+        const double c = base[tid] - ((double)most[tid] + log((sum[0] + sum[1]) + (sum[2] + sum[3])));
         base[tid] = c;
         kind[tid] = c - c == 0.0;
     }
     __syncthreads();
-    // entry e of list l
-    auto candidate = [&](uint32_t l, uint32_t e) {
+    // entry e of list l, whose key (of a beam that runs) is `key`
+    auto candidate = [&](uint32_t l, uint32_t e, uint64_t key) {
         const uint32_t beam = l / segments;
         const uint64_t row = beam * V, none = double_key(-(double)__builtin_inff());
         if (kind[beam] == 1) {
-            const uint64_t key = l * keep + e == tid ? my_key : keys[(uint64_t)l * keep + e];
             if (key == 0)
                 return Candidate{0, ~0ull};
             return Candidate{double_key(base[beam] + (double)key_value(key)), row + key_index(key)};
@@ -363,16 +358,11 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
         }
         return token < V ? Candidate{none, row + token} : Candidate{0, ~0ull};
     };
-    // If `need` lists have j + 1 candidates at or above a value each, and need (j + 1)
-    // >= keep, then nothing below it counts.  With need about half of the lists, few
-    // more than `keep` are left to order.
-    if (all > 128) {
-        uint32_t j = 0;
-        while (j + 1 < keep && (keep + j) / (j + 1) > (lists + 1) / 2)
-            ++j;
-        const uint32_t need = (keep + j) / (j + 1);
-        for (uint32_t i = tid; i < lists; i += 256)
-            ends[i] = candidate(i, j).value;
+    if (all > 64) {
+#pragma unroll
+        for (uint32_t i = 0; i < kMostLists / 256; ++i)
+            if (tid + 256 * i < lists)
+                ends[tid + 256 * i] = candidate(tid + 256 * i, j, end_key[i]).value;
         __syncthreads();
         for (uint32_t i = tid; i < lists; i += 256) {
             uint32_t above = 0, equal = 0;
@@ -392,12 +382,18 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
     auto order = [&]() {
         __syncthreads();
         const uint32_t n = count < LIST ? count : LIST;
-        for (uint32_t i = tid; i < n; i += 256) {
+        // a candidate's place is the number of those before it: four lanes, or one
+        const uint32_t lanes = n <= 64 ? 4 : 1;
+        for (uint32_t i = tid / lanes; i < n; i += 256) {
             const Candidate mine = list[i];
             uint32_t place = 0;
 #pragma unroll 4
-            for (uint32_t k = 0; k < n; ++k)
+            for (uint32_t k = tid % lanes; k < n; k += lanes)
                 place += list[k].before(mine);
+            if (lanes == 4) {
+                place += __shfl_xor(place, 1);
+                place += __shfl_xor(place, 2);
+            }
             if (place < keep)
                 sorted[place] = mine;
         }
@@ -411,10 +407,9 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
             worst = sorted[keep - 1];
         __syncthreads();
     };
-    for (uint32_t from = 0; from < all; from += 256) {
-        const uint32_t q = from + tid;
+    auto offer = [&](uint32_t q, uint64_t key) {
         if (q < all) {
-            const Candidate c = candidate(q / keep, q % keep);
+            const Candidate c = candidate(q / keep, q % keep, key);
             if (c.value != 0 && c.value >= bound && c.before(worst))
                 list[atomicAdd(&count, 1u)] = c;
         }
@@ -423,7 +418,13 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
         __syncthreads();
         if (n > LIST - 256)
             order();
-    }
+    };
+#pragma unroll
+    for (uint32_t i = 0; i < FIRST; ++i)
+        if (256 * i < all)
+            offer(tid + 256 * i, my_key[i]);
+    for (uint32_t from = 256 * FIRST; from < all; from += 256)
+        offer(from + tid, from + tid < all ? keys[from + tid] : 0);
     order();
     if (tid < keep) {
         const bool have = tid < kept;
@@ -454,7 +455,7 @@ static uint32_t beam_segments(const rnn_beam_desc &d, uint32_t &packs)
 size_t beam_workspace(const rnn_beam_desc &d)
 {
     uint32_t packs;
-    return (size_t)d.batch * d.beams * beam_segments(d, packs) * (sizeof(Total) + 8 * (size_t)d.keep);
+    return (size_t)d.batch * d.beams * beam_segments(d, packs) * (4 * sizeof(Total) + 8 * (size_t)d.keep);
 }
 
 template <class T> static int beam_go(const BeamArgs &a, hipStream_t s)

@@ -157,6 +157,25 @@ __device__ __forceinline__ float wave_sum(float v)
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
+// The sum of the lanes up to this one.
+__device__ __forceinline__ double sums_up_to(double v)
+{
+    auto with = [&](auto ctrl, auto rows) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, v);
+        auto moved = [&](uint32_t half) {
+            return (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)half, decltype(ctrl)::value,
+                                                                   decltype(rows)::value, 0xF, false);
+        };
+        v += __builtin_bit_cast(double, moved((uint32_t)(u >> 32)) << 32 | moved((uint32_t)u));
+    };
+    with(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});   // from the lane 1 before
+    with(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});   // 2
+    with(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});   // 4
+    with(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});   // 8
+    with(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row 0 to 1, 2 to 3
+    with(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // rows 0, 1 to 2, 3
+    return v;
+}
 constexpr uint32_t kInfBits = 0x7F800000u;
 
 // Four values to four 8-bit integers in a word; a row without a factor (zero,

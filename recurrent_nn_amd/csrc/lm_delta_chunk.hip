@@ -118,26 +118,6 @@ __device__ __forceinline__ Place place_in(uint32_t each)
     return {i / each * 8 + blockIdx.x % 8, i % each};
 }
 
-// The sum of the lanes up to this one.
-__device__ __forceinline__ double sums_up_to(double v)
-{
-    auto with = [&](auto ctrl, auto rows) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, v);
-        auto moved = [&](uint32_t half) {
-            return (uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)half, decltype(ctrl)::value,
-                                                                   decltype(rows)::value, 0xF, false);
-        };
-        v += __builtin_bit_cast(double, moved((uint32_t)(u >> 32)) << 32 | moved((uint32_t)u));
-    };
-    with(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});   // from the lane 1 before
-    with(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});   // 2
-    with(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});   // 4
-    with(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});   // 8
-    with(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row 0 to 1, 2 to 3
-    with(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // rows 0, 1 to 2, 3
-    return v;
-}
-
 template <class T, int KB, bool DIRECT>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSpan sp)
 {
