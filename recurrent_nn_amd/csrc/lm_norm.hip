@@ -5,7 +5,8 @@
 //
 // Bound by HBM: x and z read once, y written once.  A group stays in registers
 // between its sum and its outputs (8 KEEP elements a thread, x and z; what is
-// longer is read again, from the L2).
+// longer is read again, from the L2).  8192 x 32 x 128 in bf16 40 us, 5.0 TB/s, where
+// a copy reaches 5.15; 64 x 5001 in f16 4 us, a launch and three trips to memory.
 #include <type_traits>
 
 #include "lm_common.h"
@@ -23,10 +24,10 @@ template <int L> __device__ __forceinline__ float lanes_sum(float v)
     };
     with(std::integral_constant<int, 0xB1>{});          // lane xor 1
     with(std::integral_constant<int, 0x4E>{});          // lane xor 2
-    if (L > 4) {
+    if (L > 4)
         with(std::integral_constant<int, 0x141>{});     // half mirror
+    if (L > 8)
         with(std::integral_constant<int, 0x140>{});     // row mirror
-    }
     return v;
 }
 
@@ -96,11 +97,27 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(Nor
         const float some = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
         sum += S != WHOLE || p.skip == 0 ? some : 0.0f;
     };
+    // A single pack's weights before the sum too: 262144 x 128 in bf16 38.3 us against
+    // 40.2, 65536 x 512 39.1 and 41.0.  Of two packs, where lanes may have one, not:
+    // 246723 x 136 62 us against 56.
+    constexpr bool EARLY = KEEP == 1;
+    float weights[8];
+    auto weights_of = [&](const Part &p, float (&weight)[8]) {
+        if (S != SHORT) {
+            __builtin_memcpy(weight, w + p.start, sizeof(weight));
+        } else {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                weight[v] = __uint_as_float(w[p.start + v > 0 ? p.start + v : 0]);
+        }
+    };
     Part keep[KEEP], gate[KEEP];
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
         keep[k] = at(x, lane + THREADS * k);
         gate[k] = gated ? at(z, lane + THREADS * k) : keep[k];
+        if (EARLY)
+            weights_of(keep[k], weights);
     }
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
@@ -118,18 +135,11 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(Nor
             sum += part[i];
     }
     const float r = 1.0f / sqrtf(sum / (float)dim + a.d.eps);
-    auto put = [&](const Part &p, const Part &g) {
+    auto put = [&](const Part &p, const Part &g, const float (&weight)[8]) {
         if (p.skip >= 8)
             return;
-        float f[8], weight[8];
+        float f[8];
         values(p, g, f);
-        if (S != SHORT) {
-            __builtin_memcpy(weight, w + p.start, sizeof(weight));
-        } else {
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-                weight[v] = __uint_as_float(w[p.start + v > 0 ? p.start + v : 0]);
-        }
         Pack<T, 8> out;
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
@@ -148,10 +158,16 @@ __global__ __launch_bounds__(THREADS > 256 ? THREADS : 256) void norm_kernel(Nor
         }
     };
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        put(keep[k], gate[k]);
-    for (int i = lane + THREADS * KEEP; i < packs; i += THREADS)
-        put(at(x, i), at(z, i));
+    for (int k = 0; k < KEEP; ++k) {
+        if (!EARLY)
+            weights_of(keep[k], weights);
+        put(keep[k], gate[k], weights);
+    }
+    for (int i = lane + THREADS * KEEP; i < packs; i += THREADS) {
+        const Part p = at(x, i), g = at(z, i);
+        weights_of(p, weights);
+        put(p, g, weights);
+    }
 }
 
 template <class T, int THREADS, int KEEP> static int norm_groups_go(const NormArgs &a, hipStream_t s)
@@ -170,19 +186,35 @@ template <class T, int THREADS, int KEEP> static int norm_groups_go(const NormAr
     return (int)hipGetLastError();
 }
 
+// The fewest threads that hold a group in one pack each, or in two.  bf16 (f32), 2^25
+// elements, the time taken against the next best: 32 elements 4 threads 46 (79) us
+// against 16's 128 (125); 64 elements 8 threads 38 (75); 128 elements 16 threads 40 (80)
+// against 64's 49 (81); 256 elements two packs of 16 threads 40 (80) against 64's 69
+// (78); 512 elements 64 threads 39 (75) against four packs of 16 48 (88); 1024 elements
+// two packs of 64 threads 40 (79) against 256's 61 (74), and 520 elements 56 (81) against
+// 111 (120); 2048 elements 256 threads 40 (72) against four packs of 64 47 (89); 4096
+// elements two packs of 256 threads 40 (77) against 1024's 63 (84); 8192 elements 1024
+// threads 39 (74) against four packs of 256 48 (87), and 16384 elements, half of them read
+// twice, 44 (90) against 51 (106).  Few groups of 513 to 1024 elements take 256 threads,
+// as the chip has compute units to spare: 64 x 1024 3.1 us against 4.2; 1000 x 1024 4.3
+// and 4.4.
 template <class T> static int norm_go(const NormArgs &a, hipStream_t s)
 {
     if (a.d.dim <= 32)
         return norm_groups_go<T, 4, 1>(a, s);
+    if (a.d.dim <= 64)
+        return norm_groups_go<T, 8, 1>(a, s);
     if (a.d.dim <= 128)
         return norm_groups_go<T, 16, 1>(a, s);
     if (a.d.dim <= 256)
         return norm_groups_go<T, 16, 2>(a, s);
     if (a.d.dim <= 512)
         return norm_groups_go<T, 64, 1>(a, s);
+    if (a.d.dim <= 1024 && a.d.rows * a.d.groups > 1024)
+        return norm_groups_go<T, 64, 2>(a, s);
     if (a.d.dim <= 2048)
-        return norm_groups_go<T, 64, 4>(a, s);
-    return a.d.dim <= 8192 ? norm_groups_go<T, 256, 4>(a, s) : norm_groups_go<T, 1024, 4>(a, s);
+        return norm_groups_go<T, 256, 1>(a, s);
+    return a.d.dim <= 4096 ? norm_groups_go<T, 256, 2>(a, s) : norm_groups_go<T, 1024, 1>(a, s);
 }
 
 int launch_norm(const NormArgs &a, hipStream_t s)

@@ -32,6 +32,10 @@ NORM = [  # rows, groups, dim, dtype, gate, shared weight, pad
     (2, 1, 2048, F32, "after", True, 0), (2, 2, 2049, F16, None, False, 1), (3, 1, 5001, BF16, "before", True, 7),
     (2, 1, 8192, F32, "after", True, 0), (2, 1, 9001, F16, "after", True, 0), (1, 1, 40000, F32, "before", True, 0),
     (1, 2, 70001, BF16, "after", False, 1), (1000, 1, 16, F32, "after", True, 0),
+    (33, 3, 40, BF16, "after", True, 0), (65, 1, 63, F16, "before", True, 1), (9, 7, 72, F32, "after", False, 0),
+    (350, 3, 600, BF16, "after", True, 0), (513, 2, 1023, F16, "before", True, 1), (3, 2, 1024, F32, None, True, 0),
+    (1024, 1, 513, BF16, "after", True, 3), (2, 1, 1500, BF16, "after", True, 0), (2, 1, 3001, F32, "before", True, 1),
+    (3, 1, 4096, F16, "after", True, 0), (2, 1, 4097, BF16, "after", True, 0), (1, 1, 16384, BF16, None, True, 0),
 ]
 
 
@@ -107,7 +111,7 @@ def check_beam(got, x, scores, keep, ended=None, eos=0):
     assert np.array_equal(got.parents.cpu().numpy(), p) and np.array_equal(got.tokens.cpu().numpy(), t)
     # the normaliser: exponentials of 2 to 3 roundings, summed in 64 bits by eights
     # (3 more), and the value's own rounding
-    top = max(1.0, np.abs(d := x.float().nan_to_num(0, 0, 0)).max().item())
+    top = max(1.0, x.float().nan_to_num(0, 0, 0).abs().max().item())
     assert_close(got.scores, s, 2 * U * (8 + 2 * top) + np.abs(np.nan_to_num(s, posinf=0, neginf=0)) * U, "scores")
 
 
