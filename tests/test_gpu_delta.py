@@ -1,11 +1,14 @@
 """The gated delta rule on the GPU against its plain 64-bit definition
 (tests/delta_ref.py), within bounds that count the roundings of a float32
 evaluation."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import recurrent_nn_amd as ra
+from recurrent_nn_amd import _lib
 from tests import delta_ref
 from tests.lm_ref import HALF_STEP, U, assert_close
 from tests.test_gpu_lm import BF16, F16, F32, INF, NAN, Draw, cuda
@@ -314,12 +317,101 @@ def test_offsets_beyond_32_bits():
     """Steps 2^28 elements apart: offsets pass 2^32 bytes and 2^31 elements."""
     steps, stride = 20, 1 << 28
     x = case(Draw(21), 1, steps, 1, 1, 32, 32, BF16, "log", True, False, False)
+    far_apart(x, steps, stride)
+
+
+def far_apart(x, steps, stride):
     big = torch.empty(stride * (steps - 1) + 32 * 3, dtype=BF16, device="cuda")
     dev = on_device(x)
-    o, S = ra.gated_delta(**dev)
     for i, n in enumerate(("q", "k", "v")):
         view = big.as_strided((1, steps, 1, 32), (0, stride, 32, 1), 32 * i)
         view.copy_(dev[n])
         dev[n] = view
-    a, b = ra.gated_delta(**dev)
-    assert torch.equal(a, o) and torch.equal(b, S)
+    got, end = ra.gated_delta(**dev)
+    o, err, S, S_err = expected(x)
+    assert_close(got, o, err, "o")
+    assert_close(end, S, S_err, "state")
+
+
+@pytest.mark.parametrize("stride", [(1 << 24) - 65536 - 8, (1 << 24) - 65536])
+def test_offsets_beyond_32_bits_in_chunks(stride):
+    """The widest steps that chunks take (a chunk's rows within 2^31 bytes), and the first that they do not."""
+    far_apart(case(Draw(22), 1, 300, 1, 1, 32, 32, BF16, "log", True, False, False), 300, stride)
+
+
+def test_a_row_alone_is_as_in_a_batch():
+    """Bit for bit, on either side of every rule on the number of heads."""
+    for steps in (7, 12, 17, 40, 130):
+        x = case(Draw(30 + steps), 24, steps, 2, 4, 64, 48, BF16, "raw", True, True, False)
+        dev = on_device(x)
+        o, S = ra.gated_delta(**dev)
+        for i in (0, 23):
+            one = {n: v[i:i + 1] if n in ("q", "k", "v", "beta", "g", "state") else v for n, v in dev.items()}
+            a, b = ra.gated_delta(**one)
+            assert torch.equal(a[0], o[i]) and torch.equal(b[0], S[i]), steps
+
+
+WIDE = [  # more slices of 16 columns than compute units; batch, steps, key heads, heads, key dim, value dim, ...
+    (6, 150, 4, 8, 128, 96, BF16, "raw", True, True, True, 0),
+    (9, 70, 8, 8, 64, 72, F32, "log", False, True, True, 0),         # a last slice of 8
+    (5, 129, 4, 8, 96, 100, F16, "raw", True, True, False, 8),       # of 4
+    (17, 100, 4, 4, 40, 77, F32, "raw", True, False, True, 1),       # of 13
+    (40, 65, 1, 2, 128, 49, BF16, "log", False, True, True, 1),
+    (11, 90, 4, 8, 192, 56, BF16, "raw32", True, True, False, 0),
+    (11, 66, 4, 8, 192, 47, F32, "log", True, True, True, 3),
+    (11, 66, 8, 8, 256, 48, F16, "raw", True, True, True, 0),        # of keys too long for two slices
+]
+
+
+@pytest.mark.parametrize("k", range(len(WIDE)))
+def test_many_heads(k):
+    *shape, pad = WIDE[k]
+    x = case(Draw(700 + k), *shape)
+    o, err, S, S_err = expected(x)
+    got, end = ra.gated_delta(**on_device(x, pad))
+    assert_close(got, o, err, "o")
+    assert_close(end, S, S_err, "state")
+
+
+@pytest.mark.parametrize("dtype,ragged,b", [(BF16, False, 5), (F32, True, 2), (F16, False, 3)])
+def test_more_chunks_than_are_prepared_at_once(dtype, ragged, b):
+    """Parts of a sequence that each fit into the workspace are the sequence: every
+    part goes on from the one before, also where a row has ended."""
+    steps, h, d = 2300, 40, 128
+    x = case(Draw(50), b, steps, h, h, d, d, dtype, "log", False, True, False)
+    dev = on_device(x)
+    if ragged:
+        dev["sequence_lens"] = torch.tensor([900, steps], dtype=torch.int32, device="cuda")
+    o, S = ra.gated_delta(**dev)
+    # without a state at the end, which the parts between hand on all the same
+    desc = _lib.rnn_delta_desc(batch=b, steps=steps, key_heads=h, heads=h, key_dim=d, value_dim=d,
+                               dtype=(F32, BF16, F16).index(dtype), gate_dtype=(F32, BF16, F16).index(F32 if
+                               dev["g"].dtype == F32 else dtype), scale=d ** -0.5)
+    for n in "qkvo":
+        setattr(desc, n + "_batch_stride", steps * h * d)
+        setattr(desc, n + "_step_stride", h * d)
+        setattr(desc, n + "_head_stride", d)
+    for n in ("beta", "g"):
+        setattr(desc, n + "_batch_stride", steps * h)
+        setattr(desc, n + "_step_stride", h)
+    size = ctypes.c_size_t()
+    assert _lib.load().rnn_delta_workspace_size(ctypes.addressof(desc), ctypes.byref(size)) == 0
+    assert size.value > 200 << 20
+    space, other = torch.empty(size.value, dtype=torch.uint8, device="cuda"), torch.empty_like(o)
+    at = {n: t.data_ptr() for n, t in dev.items() if isinstance(t, torch.Tensor)}
+    assert _lib.load().rnn_delta_run(
+        ctypes.addressof(desc), torch.cuda.current_stream().cuda_stream, space.data_ptr(), size.value, at["q"],
+        at["k"], at["v"], at["beta"], at["g"], None, None, at["state"], at.get("sequence_lens"),
+        other.data_ptr(), None) == 0
+    assert torch.equal(other, o)
+    parts, at, state = [], 0, dev["state"]
+    while at < steps:
+        n = min(512, steps - at)
+        one = {k: v[:, at:at + n] if k in ("q", "k", "v", "beta", "g") else v for k, v in dev.items()}
+        one["state"] = state
+        if ragged:
+            one["sequence_lens"] = (dev["sequence_lens"] - at).clamp(0, n).to(torch.int32)
+        a, state = ra.gated_delta(**one)
+        parts.append(a)
+        at += n
+    assert torch.equal(torch.cat(parts, 1), o) and torch.equal(state, S)
