@@ -516,18 +516,18 @@ typedef struct rnn_delta_desc {
  * by sqrt(sum x^2 + RNN_DELTA_KEY_EPS).  S = state_in (NULL = zeros) before the
  * first step, state_out (nullable) = S after the last one.  One new token is a
  * call with steps = 1.
- *   Longer calls take their steps in chunks of 64, whose corrections solve a
+ *   Calls of more than 8 steps take them in chunks of 64, whose corrections solve a
  *   triangular system: the same sums in another order, so that a key, value or gate
  *   that is not finite reaches the outputs of its head from its chunk's first step
- *   on.  A row's result does not depend on the other rows, but the choice between
- *   chunks and single steps is made for the whole call.
+ *   on.  A row's result does not depend on the other rows, nor on how many there are.
  *   g, A (needs g), dt_bias (needs A), state_in, sequence_lens, state_out may be NULL.
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0,
  *   key_dim outside 1 to RNN_DELTA_MAX_KEY_DIM, key_heads that do not divide
  *   heads, an unknown dtype, a scale that is not finite, a missing or misaligned
  *   tensor, o on an input, a workspace missing, too small or misaligned;
  *   RNN_ERR_UNSUPPORTED for 2^31 steps or more, or 2^32 or more threads (64 for 32
- *   columns of a state; 256 for a head's chunk of 64 steps).
+ *   columns of a state; in chunks 512 for 16 or 32 columns of a state, and 256 for
+ *   each chunk of a head that 256 MB of workspace hold at once).
  */
 rnn_status rnn_delta_workspace_size(const rnn_delta_desc *desc, size_t *bytes);
 rnn_status rnn_delta_run(const rnn_delta_desc *desc, void *hip_stream, void *workspace,
@@ -558,8 +558,8 @@ typedef struct rnn_norm_desc {
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, dtype,
  *   eps or strides outside their ranges, gate_first without z, a missing or
  *   misaligned tensor; RNN_ERR_UNSUPPORTED for a dim of 2^30 or more, or 2^32 or
- *   more threads (4, 16, 64, 256 or 1024 a group: up to 64, 256, 2048, 16384 or
- *   more elements).
+ *   more threads (4, 8, 16, 64, 256 or 1024 a group: up to 32, 64, 256, 1024, 4096
+ *   or more elements).
  */
 rnn_status rnn_gated_norm(const rnn_norm_desc *desc, void *hip_stream, const void *x,
                           const float *weight, const void *z, void *y);
