@@ -13,6 +13,11 @@
 // float32 would decide between them.  Sums are taken in the order of the entries,
 // whatever a row's alignment, so that equal beams have equal values and their
 // candidates the order of the beams.
+//
+// 32 requests of 8 beams over 131072 entries in bf16 (67 MB, 13 us): 17.8 us, of which 7
+// are the sums' own instructions (the vector unit is busy 40% of the cycles), and 5.2 us for
+// the join, a chain of a read, the sums and the ranks.  One request of 4 beams over 100001
+// in f32: 7.2 and 6.9 us, a few trips to memory each and the launch.
 #include <type_traits>
 
 #include "lm_order.h"
@@ -437,7 +442,10 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a, uint32_t seg
 }
 
 // Segments of a row: as many as bring about 512 workgroups, of 8192 entries or more
-// each, and no more lists than the join orders well.
+// each, and no more lists than the join orders well.  Both kernels' time, us: 512
+// workgroups against 256 and 1024: 32 x 8 beams x 131072 bf16 24.4, 26.9, 26.8; 8 x 5 x
+// 262144 18.5, 18.3, 23.4.  8192 entries against 4096 and 16384: 1 x 4 x 100001 f32 14.0,
+// 15.8, 14.4; 1 x 16 x 32000 bf16 14.6, 18.6, 14.2; 128 x 4 x 8000 f16 13.5, 13.7, 14.9.
 static uint32_t beam_segments(const rnn_beam_desc &d, uint32_t &packs)
 {
     const int64_t all = (d.vocab + 7) / 8, rows = d.batch * d.beams;

@@ -10,7 +10,10 @@
 // step:  u = b (v - D k^T S),  o = scale (D q^T S + (q . k) u),  S = D S + k u^T.
 // Norms of q and k are factors of these sums, and come with the same reduction.
 //
-// A single token is bound by HBM: its state read once and written once.
+// A single token is bound by HBM: its state read once and written once.  64 tokens x
+// 32 heads x 128 x 128, 270 MB, 62 us, 4.4 TB/s; all of a wave's rows are asked for
+// before the first is used (16 KB a wave).  Each further step of a call is a chain
+// through the reduction, 2.1 us.
 #include "lm_delta.h"
 
 namespace rnnamd {
