@@ -614,8 +614,9 @@ typedef struct rnn_reorder_item {
  * RNN_REORDER_MAX_BEAMS): only rows that change are read and written.
  *   Any alignment of the tensors.  `items` is a HOST array, read during the call.
  *   Errors (nothing is enqueued): RNN_ERR_INVALID_INPUT for sizes below 0, a
- *   missing tensor, an item whose out overlaps its in otherwise, in place with
- *   keep other than beams; RNN_ERR_UNSUPPORTED for more than RNN_REORDER_MAX_BEAMS
+ *   missing tensor, an item whose out overlaps its in otherwise, another item or
+ *   parents (items run beside each other; several may read one tensor), in place
+ *   with keep other than beams; RNN_ERR_UNSUPPORTED for more than RNN_REORDER_MAX_BEAMS
  *   beams in place, or 2^32 or more threads for 32 items (one for 16 bytes of
  *   `beams` rows).
  */

@@ -3,8 +3,10 @@
 // launches on the caller's stream.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <vector>
 
 #include "lm_checks.h"
 #include "lm_common.h"
@@ -89,6 +91,25 @@ void check_beam(const rnn_beam_desc *d)
     strides("logits", d->batch, d->logits_batch_stride, d->beams, d->logits_beam_stride, d->vocab);
     if (d->vocab >= ((int64_t)1 << 31) - 65536)
         unsupported("vocab of 2^31 - 2^16 or more");
+}
+
+// What a call reads or writes, from its first byte to behind its last.
+struct Stretch {
+    uintptr_t from, to;
+    bool written;
+};
+
+// What is written lies on nothing else.
+void apart(std::vector<Stretch> &all)
+{
+    std::sort(all.begin(), all.end(), [](const Stretch &x, const Stretch &y) { return x.from < y.from; });
+    uintptr_t read = 0, written = 0;            // the ends so far
+    for (const Stretch &s : all) {
+        if (s.from < written || (s.written && s.from < read))
+            invalid("an item's out overlaps another item or parents");
+        uintptr_t &end = s.written ? written : read;
+        end = std::max(end, s.to);
+    }
 }
 
 }  // namespace
@@ -246,6 +267,9 @@ extern "C" rnn_status rnn_reorder_states(void *hip_stream, int64_t batch, int64_
         pointer("parents", parents, 4, some);
         if (count > 0 && !items)
             invalid("items are required");
+        std::vector<Stretch> all;
+        all.reserve(2 * count + 1);
+        all.push_back({(uintptr_t)parents, (uintptr_t)parents + (uintptr_t)(4 * batch * keep), false});
         for (int64_t i = 0; i < count; ++i) {
             const rnn_reorder_item &it = items[i];
             size_of("outer", it.outer);
@@ -268,7 +292,11 @@ extern "C" rnn_status rnn_reorder_states(void *hip_stream, int64_t batch, int64_
                        (uintptr_t)it.out < (uintptr_t)it.in + (uintptr_t)from) {
                 invalid("out overlaps in");
             }
+            all.push_back({(uintptr_t)it.out, (uintptr_t)it.out + (uintptr_t)to, true});
+            if (it.in != it.out)
+                all.push_back({(uintptr_t)it.in, (uintptr_t)it.in + (uintptr_t)from, false});
         }
+        apart(all);
         if (!some)
             return;
         ReorderArgs a{batch, beams, keep, parents, 0, {}, {}};

@@ -201,7 +201,8 @@ def reorder_states(states: Sequence[torch.Tensor], parents, dim: Union[int, Sequ
     device (values outside [0, beams) are taken as the nearest end), as
     :func:`beam_select` gives them.  All tensors go in one launch for up to 32.
     ``out``: tensors for the results; a state's own (keep = beams) is reordered
-    in place, and only rows that change are touched.
+    in place, and only rows that change are touched.  No result may lie on
+    another state or result.
     """
     states = list(states)
     out = None if out is None else list(out)

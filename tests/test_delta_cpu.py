@@ -186,6 +186,31 @@ def test_reorder_refusals():
     assert run_reorder([(0, 0, 1, 8)], batch=0, parents=0) == OK
 
 
+def test_reorder_items_on_each_other_are_refused():
+    """Items run beside each other: a result where another item, or the choice of rows,
+    is read or written would depend on which comes first.  (An item that no launch takes
+    stands last, so that nothing runs; rows of 8 bytes, 48 an item, 24 the parents.)"""
+    def at(i, o):
+        return (FAKE + i, FAKE + o, 1, 8)
+
+    def run(items, parents=FAKE + (1 << 20)):
+        return run_reorder([*items, (1 << 45, 1 << 46, 1 << 20, 1 << 20)], parents=parents)
+
+    for items in ([at(0, 48), at(48, 96)], [at(48, 96), at(0, 48)], [at(0, 48), at(48, 0)], [at(0, 48), at(96, 48)],
+                  [at(0, 0), at(0, 0)], [at(0, 0), at(0, 48)], [at(0, 48), at(96, 144), at(200, 136)],
+                  [at(0, 48), at(95, 200)], [at(0, 48), at(200, 1)],
+                  [at(1000 * k, 1000 * k + 48) for k in range(50)] + [at(60000, 47)]):
+        assert run(items) == INVALID, items
+    for place in (48, 28, 92):
+        assert run([at(0, 48)], FAKE + place) == INVALID, place
+    for place in (0, 24, 96):
+        assert run([at(0, 48)], FAKE + place) == UNSUPPORTED, place
+    for items in ([at(0, 48), at(0, 96)], [at(0, 72), at(24, 120)], [at(0, 0), at(48, 48)], [at(0, 48), at(96, 144)],
+                  [at(0, 48), (FAKE + 48, FAKE + 48, 1, 0)], [at(1000 * k, 1000 * k + 48) for k in range(50)]):
+        assert run(items) == UNSUPPORTED, items
+
+
+
 # ---------------------------------------------------------------------------
 # The binding
 # ---------------------------------------------------------------------------
