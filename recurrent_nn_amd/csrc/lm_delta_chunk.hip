@@ -30,14 +30,13 @@
 // w with i = 32 (w / 2) + 8 (m / 4) + 4 (w % 2) + m % 4, so that the tiles 2 p and
 // 2 p + 1 together are an operand of 32 rows; likewise rows of the state.
 //
-// One row of 8192 steps, 32 heads over 16 key heads, 128 x 128, bf16: 67 us and 265 us.
+// One row of 8192 steps, 32 heads over 16 key heads, 128 x 128, bf16: 90 us and 240 us.
 // The first kernel's chunks are independent; their chains (the forward substitution, LDS
-// between the steps) leave it waiting half of its cycles, the matrix cores busy 8% of
-// them.  The second is a chain along the chunks, 2.1 us each on every compute unit: 1.2 us
-// of it are the products and LDS between them (157 us in all with every load taken out),
-// the rest is the reading of 88 KB of operands a chunk by each of a head's eight
-// workgroups from the L2, 3.2 GB at 12 TB/s (loads taken out by kind: T 48 us, K as it is
-// and values 58, K transposed 24, Q and P 53).  The matrix cores are busy 15%.
+// between the steps) and 0.23 GB that it writes bound it, the matrix cores are busy 6% of
+// it.  The second is a chain along the chunks, 1.9 us each on every compute unit: 1.2 us of
+// it are the products and LDS between them (157 us in all with every load taken out), the
+// rest is the reading of 88 KB of operands a chunk by each of a head's eight workgroups
+// from the L2, 3.2 GB at 13 TB/s.  The matrix cores are busy 16%.
 #include <type_traits>
 
 #include "lm_delta.h"
@@ -363,8 +362,9 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
         for (int s = 0; s < 3; ++s)
             out.put(s, to + s * kFragment);
     }
-    // K transposed: eight steps of a row of the state a lane
-    if (head % each == 0)
+    // K transposed: eight steps of a row of the state a lane (by the last of a key head's
+    // heads; the first one has left the operands of K and Q)
+    if (head % each == each - 1)
         for (int item = tid; item < 4 * KB * 64; item += 256) {
             const int l = item % 64, f = item / 64, tile = f / 2, p = f % 2;
             const int r = row_of(tile, l % 16), i = 32 * p + 8 * (l / 16);
@@ -850,11 +850,11 @@ template <class T, int KB> static uint64_t span_of(const rnn_delta_desc &d, bool
 }
 
 // Two tiles of columns a workgroup where one would be more workgroups than compute
-// units: a workgroup's chain is longer, but the operands are read half as often.  bf16,
-// 128 x 128, two against one: 2 rows of 4096 steps of 32 heads 181 us against 279, 8 of
-// 1024 195 and 300, one of 48 heads 337 and 539; one of 32 heads (256 workgroups) 317
-// and 274.  f32, 64 x 64, 8 rows of 1000 steps: 16 heads 66 and 94, 8 heads (256) 46 and 40.
-// Keys beyond 192 do not fit the registers twice.
+// units: a workgroup's chain is longer, but the operands are read half as often.  The
+// second kernel, bf16, 128 x 128, two against one: 2 rows of 4096 steps of 32 heads 180 us
+// against 255, 8 of 1024 201 and 284, one of 48 heads 342 and 460; one of 32 heads (256
+// workgroups) 320 and 245.  f32, 64 x 64, 8 rows of 1000 steps: 16 heads 70 and 100, 8
+// heads (256) 38 and 31.  Keys beyond 192 do not fit the registers twice.
 static bool wide_slices(const rnn_delta_desc &d)
 {
     return d.key_dim <= 192 && d.batch * d.heads * ((d.value_dim + 15) / 16) > 256;
@@ -881,8 +881,9 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
         if (rc)
             return rc;
         const dim3 grid((uint32_t)(rounds * 8 * slices)), block(512);
-        if (!wide)
-            delta_chunks_kernel<T, KB, DIRECT, 1><<<grid, block, 0, s>>>(a, sp, (uint32_t)slices);
+        if constexpr (!DIRECT)
+            if (!wide)
+                delta_chunks_kernel<T, KB, DIRECT, 1><<<grid, block, 0, s>>>(a, sp, (uint32_t)slices);
         if constexpr (KB <= 6)
             if (wide)
                 delta_chunks_kernel<T, KB, DIRECT, 2><<<grid, block, 0, s>>>(a, sp, (uint32_t)slices);
@@ -893,16 +894,22 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
     return 0;
 }
 
-// f(type, blocks of 32 rows of the state, whether keys and queries are operands as
-// they are)
+// f(type, blocks of 32 rows of the state, whether keys and queries are read as they are:
+// bfloat16 of whole blocks, where two tiles of columns share what is read).  Elsewhere the
+// first kernel leaves them as operands, one after another: it writes more, but a head's
+// rows lie kilobytes apart, and each of its workgroups reads them all.  Both kernels, as
+// operands against as they are, bf16: one row of 32 heads over 16, 8192 steps 337 us
+// against 347, over 8, 4096 steps 134 and 155; 4 heads of 256 x 256, 4096 steps 173 and 213;
+// two tiles at a time 8 rows of 1024 steps 277 and 274, 2 of 4096 steps and 32 key heads
+// 297 and 275.
 template <class F> static auto with_sizes(const rnn_delta_desc &d, F &&f)
 {
     auto blocks = [&](auto type) {
         using T = decltype(type);
         auto at = [&](auto kb) {
             constexpr int KB = decltype(kb)::value;
-            if constexpr (std::is_same<T, BF16>::value)
-                if (d.key_dim == 32 * KB)
+            if constexpr (std::is_same<T, BF16>::value && KB <= 6)
+                if (d.key_dim == 32 * KB && wide_slices(d))
                     return f(type, kb, std::true_type{});
             return f(type, kb, std::false_type{});
         };
