@@ -30,9 +30,9 @@
 // w with i = 32 (w / 2) + 8 (m / 4) + 4 (w % 2) + m % 4, so that the tiles 2 p and
 // 2 p + 1 together are an operand of 32 rows; likewise rows of the state.
 //
-// One row of 8192 steps, 32 heads over 16 key heads, 128 x 128, bf16: 90 us and 240 us.
+// One row of 8192 steps, 32 heads over 16 key heads, 128 x 128, bf16: 76 us and 245 us.
 // The first kernel's chunks are independent; their chains (the forward substitution, LDS
-// between the steps) and 0.23 GB that it writes bound it, the matrix cores are busy 6% of
+// between the steps) and 0.23 GB that it writes bound it, the matrix cores are busy 7% of
 // it.  The second is a chain along the chunks, 1.9 us each on every compute unit: 1.2 us of
 // it are the products and LDS between them (157 us in all with every load taken out), the
 // rest is the reading of 88 KB of operands a chunk by each of a head's eight workgroups
@@ -126,7 +126,7 @@ __device__ __forceinline__ Place place_in(uint32_t each)
     return {i / each * 8 + blockIdx.x % 8, i % each};
 }
 
-template <class T, int KB, bool DIRECT>
+template <class T, int KB, bool DIRECT, bool WHOLE>
 __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSpan sp)
 {
     using raw = typename T::raw;
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int col = 32 * kb + 8 * g;
-            if (DIRECT || dk == 32 * KB) {
+            if (WHOLE) {
                 v[kb] = load_pack<T, 8>(at + col);
             } else {
 #pragma unroll
@@ -178,11 +178,20 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
     load(k_at, kv);
     load(q_at, qv);
     float beta = 0.0f, log_g = 0.0f;
-    if (w == 0 && lane < here) {
-        const int64_t t = start + lane;
-        beta = gate_at<T>(a.beta, a.d.gate_dtype, b * a.d.beta_batch_stride + t * a.d.beta_step_stride + head);
-        if (a.g)
-            log_g = gate_at<T>(a.g, a.d.gate_dtype, b * a.d.g_batch_stride + t * a.d.g_step_stride + head);
+    if (w == 0 && lane < here) {                // (both under way before either is waited for)
+        const int64_t t = start + lane, beta_at = b * a.d.beta_batch_stride + t * a.d.beta_step_stride + head;
+        const int64_t g_at = a.g ? b * a.d.g_batch_stride + t * a.d.g_step_stride + head : beta_at;
+        auto gates = [&](auto type) {
+            using Gate = decltype(type);
+            const auto x = ((const typename Gate::raw *)a.beta)[beta_at];
+            const auto y = ((const typename Gate::raw *)(a.g ? a.g : a.beta))[g_at];
+            beta = Gate::load(x);
+            log_g = Gate::load(y);
+        };
+        if (a.d.gate_dtype == RNN_DTYPE_F32)
+            gates(F32{});
+        else
+            gates(T{});
     }
     v8b kf[KB][KP], qf[KB][KP];
     auto planes = [&](const Pack<T, 8> (&v)[KB], v8b (&out)[KB][KP]) {
@@ -215,6 +224,16 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
 #pragma unroll
         for (int p = 0; p < KP; ++p)
             *(v8b *)&keys[p][row][32 * kb + 8 * g] = kf[kb][p];
+    if (w == 0) {                               // gates, a step a lane
+        double sum = 0.0;
+        if (a.g && lane < here)
+            sum = log_decay(log_g, a.A != nullptr, a.A ? a.A[head] : 0.0f, a.dt_bias ? a.dt_bias[head] : 0.0f);
+        sum = sums_up_to(sum) * 1.4426950408889634074;
+        G2[lane] = {(float)sum, (float)(sum - (double)(float)sum)};
+        rates[lane] = lane < here ? rate_of(beta, a.d.beta_sigmoid) : 0.0f;
+    }
+    __syncthreads();
+    // (here, where no load is waited for any more: the wait would be for these too)
     if (!DIRECT && head % each == 0) {
         char *to = sp.packed + key_unit * (2 * Sizes::kt) + (size_t)w * KB * KP * kFragment + lane * 16;
 #pragma unroll
@@ -225,15 +244,6 @@ __global__ __launch_bounds__(256) void delta_prepare_kernel(DeltaArgs a, DeltaSp
                 *(v8b *)(to + Sizes::kt + (kb * KP + p) * kFragment) = qf[kb][p];
             }
     }
-    if (w == 0) {                               // gates, a step a lane
-        double sum = 0.0;
-        if (a.g && lane < here)
-            sum = log_decay(log_g, a.A != nullptr, a.A ? a.A[head] : 0.0f, a.dt_bias ? a.dt_bias[head] : 0.0f);
-        sum = sums_up_to(sum) * 1.4426950408889634074;
-        G2[lane] = {(float)sum, (float)(sum - (double)(float)sum)};
-        rates[lane] = lane < here ? rate_of(beta, a.d.beta_sigmoid) : 0.0f;
-    }
-    __syncthreads();
     auto apart = [&](float2 x, float2 y) { return __builtin_amdgcn_exp2f((x.x - y.x) + (x.y - y.y)); };
     if (w == 3) {
         float *vec = (float *)(sp.vec + unit * Sizes::vec);
@@ -875,8 +885,11 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
         const uint64_t count = all - first < span ? all - first : span;
         const DeltaSpan sp{(uint32_t)first, (uint32_t)count, ws + l.t, ws + l.p, ws + l.vec, ws + l.kt,
                            ws + l.packed, first == 0 ? a.state_in : between, between};
-        delta_prepare_kernel<T, KB, DIRECT>
-            <<<dim3((uint32_t)(rounds * 8 * count)), dim3(256), 0, s>>>(a, sp);
+        const dim3 units((uint32_t)(rounds * 8 * count));
+        if (DIRECT || a.d.key_dim == 32 * KB)
+            delta_prepare_kernel<T, KB, DIRECT, true><<<units, dim3(256), 0, s>>>(a, sp);
+        else if constexpr (!DIRECT)
+            delta_prepare_kernel<T, KB, DIRECT, false><<<units, dim3(256), 0, s>>>(a, sp);
         int rc = (int)hipGetLastError();
         if (rc)
             return rc;
@@ -898,8 +911,8 @@ template <class T, int KB, bool DIRECT> static int chunks_go(const DeltaArgs &a,
 // bfloat16 of whole blocks, where two tiles of columns share what is read).  Elsewhere the
 // first kernel leaves them as operands, one after another: it writes more, but a head's
 // rows lie kilobytes apart, and each of its workgroups reads them all.  Both kernels, as
-// operands against as they are, bf16: one row of 32 heads over 16, 8192 steps 337 us
-// against 347, over 8, 4096 steps 134 and 155; 4 heads of 256 x 256, 4096 steps 173 and 213;
+// operands against as they are, bf16: one row of 32 heads over 16, 8192 steps 326 us
+// against 347, over 8, 4096 steps 129 and 155; 4 heads of 256 x 256, 4096 steps 170 and 213;
 // two tiles at a time 8 rows of 1024 steps 277 and 274, 2 of 4096 steps and 32 key heads
 // 297 and 275.
 template <class F> static auto with_sizes(const rnn_delta_desc &d, F &&f)
